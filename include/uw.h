@@ -496,6 +496,181 @@ UW_API uw_status uw_mlp_stack(const uw_matrix* const* mats, const int32_t* pipel
                               size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Products grouped by expert, and products with a fused epilogue
+ * ------------------------------------------------------------------------- */
+
+#define UW_MAX_EXPERTS 1024
+#define UW_MAX_TOP_K 32
+#define UW_MAX_TOKENS (1 << 20)
+#define UW_MAX_SLOTS (1 << 22)
+
+/* In the calls from here to the autotuner, x, h, workspaces, tables and the
+ * y of a product are 16-byte aligned as everywhere; logits, biases,
+ * residuals, parts, the y of a combination and the int32 and FP32 arrays need
+ * only their element's alignment (slices of larger tensors). */
+
+/* Activation of an epilogue: ReLU; GELU v Phi(v) with the normal
+ * distribution's Phi; its tanh form; SiLU v / (1 + exp(-v)). */
+typedef enum {
+  UW_ACT_NONE = 0,
+  UW_ACT_RELU = 1,
+  UW_ACT_GELU = 2,
+  UW_ACT_GELU_TANH = 3,
+  UW_ACT_SILU = 4
+} uw_activation;
+
+typedef enum { UW_OUT_BF16 = 0, UW_OUT_FP32 = 1 } uw_out_type;
+
+/* What a product does to its FP32 sums before it stores them:
+ * y = act(sum + bias) + residual, all in FP32, rounded once (to nearest even)
+ * for UW_OUT_BF16.  bias: device BF16 [n_experts, rows] or NULL.  residual:
+ * device BF16, one row of `rows` values per row of y, or NULL; y may be the
+ * same memory as a residual of the same type (each value is read by the
+ * thread that writes it). */
+typedef struct {
+  const uint16_t* bias;
+  const uint16_t* residual;
+  int32_t activation;  /* uw_activation */
+  int32_t out_type;    /* uw_out_type: type of y */
+} uw_epilogue;
+
+/* Compressed matrices of one shape, one per expert, as the grouped products
+ * take them: `table` is a device array of n_experts records (where each
+ * matrix's pack lies, its palette) that uw_experts_init fills once at load
+ * time.  The caller owns the table and the matrices' arrays. */
+typedef struct {
+  int32_t n_experts;
+  int32_t reserved;
+  int64_t rows, cols;
+  const void* table;
+} uw_experts;
+
+/* Bytes of the device table for n_experts (0 outside 1..UW_MAX_EXPERTS). */
+UW_API size_t uw_experts_table_bytes(int32_t n_experts);
+
+/* Fill `table` (device, caller-owned, 16-byte aligned) and *out for
+ * mats[0..n_experts), which all have their direct-palette form (pack,
+ * pack_off) and the same rows and cols; each has its own palette.
+ * Synchronizes `stream`.  Errors: UW_ERR_INVALID_ARG (NULL or misaligned
+ * pointers, a matrix without its pack, n_experts), UW_ERR_UNSUPPORTED_SHAPE
+ * (different shapes), UW_ERR_CORRUPT (a layout inconsistent with itself),
+ * UW_ERR_WORKSPACE_TOO_SMALL (table_bytes), UW_ERR_NO_DEVICE, UW_ERR_CUDA. */
+UW_API uw_status uw_experts_init(const uw_matrix* const* mats, int32_t n_experts, void* table,
+                                 size_t table_bytes, uw_experts* out, void* stream);
+
+/* Workspace of the grouped products for n_rows slots (0 for invalid
+ * arguments); swiglu: nonzero for uw_gemm_grouped_swiglu. */
+UW_API size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, int32_t swiglu);
+
+/* Matrix products grouped by expert with ragged sizes (the products of a
+ * mixture of experts; the page's reconstructive GEMM, section "How the
+ * reconstructive matmul works", once per expert in one launch):
+ *   y[s] = act(x[rows[s]] W_e^T + bias[e]) + residual[s]
+ * for the slots s in [offsets[e], offsets[e+1]) of every expert e.
+ * x: device BF16 [x_rows, cols].  rows: device int32, the row of x for each
+ * slot, NULL: slot s reads row s.  offsets: device int32[n_experts + 1],
+ * rising, within [0, n_rows]; read on the device, nothing synchronizes.
+ * y: device [n_rows, rows], BF16 or FP32 (epi->out_type); epi may be NULL
+ * (plain BF16 product).  Slots outside [offsets[0], offsets[n_experts]) are
+ * left as they were.  The matrix of an expert without slots is not read.
+ * n_rows = 0 launches nothing.
+ * Sums are FP32; their order depends only on the shapes, n_rows, the offsets
+ * and the SM count.  cols <= 32768.
+ * The table and the matrices are constant (see the conventions above);
+ * offsets, rows, x, bias and residual may come from the kernel ahead.
+ * Errors: UW_ERR_INVALID_ARG (NULL or misaligned pointers, x_rows < n_rows
+ * without rows, unknown activation or type), UW_ERR_UNSUPPORTED_SHAPE,
+ * UW_ERR_WORKSPACE_TOO_SMALL, UW_ERR_NO_DEVICE, UW_ERR_CUDA; found on the
+ * device: offsets that fall or leave [0, n_rows] record UW_ERR_INVALID_ARG
+ * and nothing is computed; a row number outside [0, x_rows) records it too
+ * and that slot's values are undefined; inconsistent pack offsets record
+ * UW_ERR_CORRUPT. */
+UW_API uw_status uw_gemm_grouped(const uw_experts* w, const uint16_t* x, int32_t x_rows,
+                                 const int32_t* rows, const int32_t* offsets, int32_t n_rows,
+                                 const uw_epilogue* epi, void* y, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Gate and up products of every expert's slots with SwiGLU between them, in
+ * one launch: h[s] = bf16(SiLU(x[rows[s]] G_e^T) * (x[rows[s]] U_e^T)).  Both
+ * sums stay FP32 up to the one rounding of h (uw_mlp_block rounds g and u to
+ * BF16 first).  gate and up have the same shape and number of experts.
+ * Workspace: uw_grouped_workspace_bytes with swiglu = 1.  Otherwise as
+ * uw_gemm_grouped without an epilogue. */
+UW_API uw_status uw_gemm_grouped_swiglu(const uw_experts* gate, const uw_experts* up, const uint16_t* x,
+                                        int32_t x_rows, const int32_t* rows, const int32_t* offsets,
+                                        int32_t n_rows, uint16_t* h, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Product of one direct-palette matrix with bias, activation and residual in
+ * its epilogue: y = act(x W^T + bias) + residual, x: device BF16 [batch,
+ * cols], y: device [batch, rows] BF16 or FP32; epi may be NULL.  Unlike
+ * uw_gemm_direct_palette the batch has no limit of 512 (batch 0 launches
+ * nothing), and the order of the sums is this kernel's own.  Workspace:
+ * uw_gemm_epilogue_workspace_bytes.  Errors as uw_gemm_grouped. */
+UW_API size_t uw_gemm_epilogue_workspace_bytes(const uw_layout* L, int32_t batch);
+UW_API uw_status uw_gemm_epilogue(const uw_matrix* m, const uint16_t* x, int32_t batch,
+                                  const uw_epilogue* epi, void* y, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mixture of experts (not on the page, which compresses dense MLPs: a sparse
+ * MLP holds the same three matrices once per expert)
+ * ------------------------------------------------------------------------- */
+
+/* Router: for each token t, the top_k experts with the largest logits in
+ * falling order (equal logits: the lower expert first) and their weights, and
+ * the grouping by expert that the grouped products take.
+ *   p = softmax(logits[t]), weight = p[e], or p[e] / (sum of the chosen p)
+ *   with `renormalize`.
+ * logits: device [n_tokens, n_experts], BF16 or FP32 (logits_type).  A logit
+ * of -inf or NaN is never chosen and has p = 0; +inf counts as the largest
+ * finite value.  A token with fewer than top_k choosable experts has expert
+ * -1, weight 0 and slot -1 in the remaining places (a padded row: all -inf).
+ * Outputs (device): weights FP32 and experts, slots int32 [n_tokens, top_k];
+ * offsets int32[n_experts + 1]: expert e's slots are [offsets[e],
+ * offsets[e+1]); rows int32[n_tokens * top_k]: the token of each slot, in
+ * rising order within an expert, entries from offsets[n_experts] on left as
+ * they were.  slots[t, j]: the slot of token t's j-th choice.
+ * n_tokens 0..UW_MAX_TOKENS, top_k 1..min(n_experts, UW_MAX_TOP_K).
+ * Workspace: uw_moe_route_workspace_bytes (0 for invalid arguments).
+ * Errors: UW_ERR_INVALID_ARG, UW_ERR_WORKSPACE_TOO_SMALL, UW_ERR_NO_DEVICE,
+ * UW_ERR_CUDA. */
+UW_API size_t uw_moe_route_workspace_bytes(int32_t n_tokens, int32_t n_experts, int32_t top_k);
+UW_API uw_status uw_moe_route(const void* logits, int32_t logits_type, int32_t n_tokens,
+                              int32_t n_experts, int32_t top_k, int32_t renormalize, float* weights,
+                              int32_t* experts, int32_t* slots, int32_t* rows, int32_t* offsets,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Weighted combination of the experts' outputs:
+ *   y[t] = bf16(residual[t] + sum_j weights[t, j] * parts[slots[t, j]])
+ * in FP32, in the order of j.  parts: device [n_rows, cols], FP32 or BF16
+ * (parts_type); slots, weights: [n_tokens, top_k]; a slot outside
+ * [0, n_rows) adds nothing, whatever its weight.  residual: device BF16
+ * [n_tokens, cols] or NULL; y may be the same memory.  n_tokens = 0 launches
+ * nothing.  Errors: UW_ERR_INVALID_ARG, UW_ERR_UNSUPPORTED_SHAPE,
+ * UW_ERR_NO_DEVICE, UW_ERR_CUDA. */
+UW_API uw_status uw_moe_combine(const void* parts, int32_t parts_type, const int32_t* slots,
+                                const float* weights, int32_t n_tokens, int32_t top_k, int64_t cols,
+                                int32_t n_rows, const uint16_t* residual, uint16_t* y, void* stream);
+
+/* The sparse counterpart of uw_mlp_block: router, gate and up products with
+ * SwiGLU, down product (FP32) and weighted combination, on one stream without
+ * synchronizing: the four calls above with their intermediates in the
+ * workspace.  gate, up: experts of [ffn, d]; down: of [d, ffn]; x, y, residual
+ * (or NULL): device BF16 [n_tokens, d]; logits: [n_tokens, n_experts].
+ * y may be the residual's memory, and x's.
+ * Workspace: uw_moe_workspace_bytes (0 for invalid arguments).  Errors:
+ * UW_ERR_INVALID_ARG (NULL or misaligned pointers, shapes that do not chain),
+ * UW_ERR_WORKSPACE_TOO_SMALL, and those of the four calls. */
+UW_API size_t uw_moe_workspace_bytes(const uw_experts* gate, const uw_experts* up,
+                                     const uw_experts* down, int32_t n_tokens, int32_t top_k);
+UW_API uw_status uw_moe_block(const uw_experts* gate, const uw_experts* up, const uw_experts* down,
+                              const void* logits, int32_t logits_type, int32_t top_k,
+                              int32_t renormalize, const uint16_t* x, int32_t n_tokens,
+                              const uint16_t* residual, uint16_t* y, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Autotuner (sections "Key Points" and "Why no single pipeline wins")
  * ------------------------------------------------------------------------- */
 

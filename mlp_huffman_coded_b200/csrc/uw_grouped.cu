@@ -1,0 +1,1115 @@
+// Reconstructive GEMM over groups of rows (one compressed matrix per group)
+// with a fused epilogue: the products of a mixture of experts
+//   y[s] = act(x[rows[s]] W_e^T + b_e) + r[s],       e = the group of slot s,
+//   h[s] = SiLU(x[rows[s]] G_e^T) * (x[rows[s]] U_e^T)
+// and, with one group, the product of one matrix with bias, activation and
+// residual in its epilogue.
+//
+// Method: Cloudflare, "Unweight: how we compressed an LLM 22% without
+// sacrificing quality", section "How the reconstructive matmul works"
+// (compressed tiles staged on chip, rebuilt there, fed to the tensor cores).
+// The page speaks of one matrix; the groups and the epilogue are not on it.
+//
+// What bounds it: with few rows per group, the bytes of the active groups'
+// packs (1.502 per weight plus 2 per verbatim weight); with many, the MMA
+// rate and the rebuild of each 128 x 64 weight tile (about 320 cycles of the
+// SM's issue slots, against 2 N cycles for the four MMAs of N columns).
+//
+// Layout of the work:
+//  * W is the MMA's A operand (128 weight rows = 128 TMEM lanes), the rows of
+//    the group are the N side (16..256 columns): decode-time groups of a few
+//    rows cost one N = 16 MMA, and nothing is padded to 128 rows.
+//  * The unit of work is one 64-column k-block of one (group, 128-row tile,
+//    column tile).  Group sizes are read on the device; every CTA computes
+//    the same table of units and takes an equal contiguous share (stream-K),
+//    so ragged groups, few large tiles and many small ones balance alike.
+//    A group without rows has no units: its weights are never read.
+//  * Every ring slot carries ONE tile record (12304 bytes and its verbatim
+//    rows): it goes back to the producer as soon as that tile is rebuilt, so
+//    nearly all of the weight ring is in flight to HBM at any time.
+//  * With SwiGLU, the gate and the up tile of a k-block follow each other
+//    through the same rings and share the activation tile; both sums stay in
+//    tensor memory and meet in the epilogue, so g and u are never rounded or
+//    stored.
+//  * The rows of x arrive by TMA gather (4 row numbers per copy): the rows
+//    of a group need not be copied next to each other first.
+//  * A tile shared by several CTAs: each writes its FP32 sums to a slot of
+//    its own (a CTA has at most two such tiles, its first and its last) and
+//    takes a ticket; the last adds all of them in CTA order and runs the
+//    epilogue.  Nobody waits for another CTA; the sum does not depend on
+//    timing.
+//  * Barrier waits are bounded: a timeout records UW_ERR_TIMEOUT, drains
+//    copies and MMAs in flight, frees tensor memory and returns.
+#include <algorithm>
+#include <cstdlib>
+#include <cstring>
+#include <mutex>
+#include <vector>
+
+#include "uw_device.cuh"
+#include "uw_internal.h"
+
+namespace uw {
+
+namespace {
+
+// Warp roles: 0 = weight producer, 1 = activation producer, 2..5 = MMA
+// issuers (warp 2 owns tensor memory), 6..13 = two rebuild groups of 4 warps
+// (group g rebuilds tiles i with i % 2 == g), 14..17 = epilogue.
+constexpr int kGroups = 2;
+constexpr int kMaxIssuers = 4;
+constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 6, kWarpEpi = kWarpRebuild + 4 * kGroups;
+constexpr int kThreads = 32 * (kWarpEpi + 4);
+constexpr int kMaxSlots = 16;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBody = 12304, kBodyIdx = 8192, kBodyMask = 12288;  // pack record of a tile (uw.h)
+constexpr uint32_t kMinTail = 8;  // verbatim rows staged per tile, at least
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr size_t kSmemFloor = 120 * 1024;  // one CTA (and one owner of tensor memory) per SM
+
+// One group's share of the schedule.
+struct SchedEntry {
+  int unit0;      // first unit
+  int start;      // first slot
+  int count;      // slots
+  int n_nt;       // column tiles in bits 16.., columns per tile (multiple of 16) in bits 0..15
+};
+
+struct GParams {
+  int E, N, KB, n_mt, x_rows, n_rows;
+  int grid, cap;        // columns per tile, at most
+  int n_iss, n_acc;
+  int sx, sa, sw;       // ring slots: activations, A tiles (tensor memory), weight records
+  uint32_t x_slot_bytes, w_base, w_slot_bytes, sched_off, bar_off, a_col0;
+  int vcap;             // verbatim rows staged per record
+  int early;            // offsets are not the previous kernel's output
+  const int32_t* offsets;
+  const int32_t* rows;
+  const ExpertDesc* table[2];
+  ExpertDesc one;       // the only group's record when table[0] is NULL
+  const uint16_t* bias;
+  const uint16_t* residual;
+  int act, out_fp32;
+  void* y;
+  float* partials;
+  long long partial_stride;  // floats of one partial slot
+  uint32_t* counters;
+  uint32_t* status;
+};
+
+struct GBars {
+  uint64_t wfull[kMaxSlots], wempty[kMaxSlots];
+  uint64_t xfull[kMaxSlots], xempty[kMaxSlots];
+  uint64_t afull[kMaxSlots], aempty[kMaxSlots];
+  uint64_t acc_full[2], acc_empty[2], drain[kMaxIssuers];
+  uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
+  uint32_t tmem_base, abort, last_arriver, total;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars* b, uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, &b->abort, status));
+}
+
+// the 4 epilogue warps (named barrier 1)
+__device__ __forceinline__ bool group_and(bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return out != 0;
+}
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Four rows of a 2-D tensor map (box one row high) at column c, packed one
+// below the other.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int c, int r0, int r1, int r2, int r3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ------------------------------- schedule ------------------------------------
+// A CTA's units [u0, u1) as segments: runs of k-blocks of one (group, row
+// tile, column tile).  Every role walks the same sequence.
+struct Seg {
+  int u, u1;          // next unit, end of the CTA's share
+  int e, mt, nt;      // of the segment
+  int kb0, kb1;
+  int ntile, slot0, nvalid;
+  int tile_u;         // first unit of the whole tile
+};
+
+__device__ __forceinline__ int units_before(int c, int total, int grid) {
+  return static_cast<int>(static_cast<long long>(c) * total / grid);
+}
+// CTA whose share holds unit u
+__device__ __forceinline__ int unit_owner(int u, int total, int grid) {
+  return static_cast<int>((static_cast<long long>(u + 1) * grid - 1) / total);
+}
+
+__device__ __forceinline__ void seg_fill(Seg& s, const SchedEntry* sched, const GParams& p, int local) {
+  const SchedEntry en = sched[s.e];
+  const int n_nt = en.n_nt >> 16;
+  const int tile = local / p.KB;
+  s.kb0 = local - tile * p.KB;
+  s.mt = tile / n_nt;
+  s.nt = tile - s.mt * n_nt;
+  s.ntile = en.n_nt & 0xFFFF;
+  s.slot0 = en.start + s.nt * s.ntile;
+  s.nvalid = min(s.ntile, en.count - s.nt * s.ntile);
+  s.tile_u = s.u - s.kb0;
+  s.kb1 = min(p.KB, s.kb0 + (s.u1 - s.u));
+}
+// first segment at unit s.u (s.u < s.u1)
+__device__ __forceinline__ void seg_init(Seg& s, const SchedEntry* sched, const GParams& p, int u0, int u1) {
+  s.u = u0;
+  s.u1 = u1;
+  int lo = 0, hi = p.E;  // last entry with unit0 <= u0 (entries without units share their successor's unit0)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sched[mid].unit0 <= u0) lo = mid;
+    else hi = mid;
+  }
+  s.e = lo;
+  seg_fill(s, sched, p, u0 - sched[lo].unit0);
+}
+// false when the share is done
+__device__ __forceinline__ bool seg_next(Seg& s, const SchedEntry* sched, const GParams& p) {
+  s.u += s.kb1 - s.kb0;
+  if (s.u >= s.u1) return false;
+  while (s.u >= sched[s.e + 1].unit0) ++s.e;
+  seg_fill(s, sched, p, s.u - sched[s.e].unit0);
+  return true;
+}
+
+struct Ring {
+  int slot;
+  uint32_t use;
+};
+__device__ __forceinline__ void ring_next(Ring& r, int slots) {
+  if (++r.slot == slots) {
+    r.slot = 0;
+    ++r.use;
+  }
+}
+
+// ------------------------------- rebuild -------------------------------------
+// One thread owns one weight row of the tile: 64 BF16 values as 32 words.
+// Plain 16-byte shared-memory reads (the record's chunk order keeps them free
+// of bank conflicts); exponents come from two byte permutes per four indices.
+__device__ __forceinline__ void rebuild_row(const PaletteTables& pal, bool uniform, uint32_t body, int r,
+                                            uint32_t (&o)[32]) {
+  uint32_t iw[8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 v = lds128(body + kBodyIdx + r * 32 + ((j ^ ((r >> 2) & 1)) << 4));
+    iw[4 * j] = v.x;
+    iw[4 * j + 1] = v.y;
+    iw[4 * j + 2] = v.z;
+    iw[4 * j + 3] = v.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 s = lds128(body + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t nib = iw[2 * j + h];
+      uint32_t e0, e1;
+      if (uniform) {
+        e0 = lookup4_uniform(pal, nib);
+        e1 = lookup4_uniform(pal, nib >> 16);
+      } else {
+        e0 = lookup4_mixed(pal, nib);
+        e1 = lookup4_mixed(pal, nib >> 16);
+      }
+      rebuild4(sw[2 * h], e0, o[8 * j + 4 * h + 0], o[8 * j + 4 * h + 1]);
+      rebuild4(sw[2 * h + 1], e1, o[8 * j + 4 * h + 2], o[8 * j + 4 * h + 3]);
+    }
+  }
+}
+
+__device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
+  const uint4 a = *reinterpret_cast<const uint4*>(&d->lo0);
+  const uint4 b = *reinterpret_cast<const uint4*>(&d->b7lo0);
+  PaletteTables t;
+  t.lo0 = a.x;
+  t.lo1 = a.y;
+  t.hi0 = a.z;
+  t.hi1 = a.w;
+  t.b7lo0 = b.x;
+  t.b7lo1 = b.y;
+  t.b7hi0 = b.z;
+  t.b7hi1 = b.w;
+  t.keep = d->keep;
+  return t;
+}
+
+// ------------------------------- epilogue ------------------------------------
+// FP32 throughout; the only rounding is the store's.  The GELU forms are
+// written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case UW_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
+    case UW_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case UW_ACT_GELU_TANH: {
+      const float t = 1.5957691216057308f * (v + 0.044715f * v * v * v);  // 2 sqrt(2 / pi) (...)
+      return v / (1.0f + expf(-t));
+    }
+    case UW_ACT_SILU: return v / (1.0f + expf(-v));
+    default: return v;
+  }
+}
+
+// ------------------------------- the kernel ----------------------------------
+template <int NMAT>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ GParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t smem_s = smem_u32(smem);
+  GBars* bars = reinterpret_cast<GBars*>(smem + p.bar_off);
+  SchedEntry* sched = reinterpret_cast<SchedEntry*>(smem + p.sched_off);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ---- set-up: barriers, tensor memory and the table of units
+  if (warp == kWarpW && lane == 0) {
+    for (int s = 0; s < p.sw; ++s) {
+      mbar_init(&bars->wfull[s], 1);
+      mbar_init(&bars->wempty[s], 4);
+    }
+    for (int s = 0; s < p.sx; ++s) {
+      mbar_init(&bars->xfull[s], 1);
+      mbar_init(&bars->xempty[s], NMAT);
+    }
+    for (int s = 0; s < p.sa; ++s) {
+      mbar_init(&bars->afull[s], 4);
+      mbar_init(&bars->aempty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->acc_full[i], p.n_iss);
+      mbar_init(&bars->acc_empty[i], 4);
+    }
+    for (int i = 0; i < kMaxIssuers; ++i) mbar_init(&bars->drain[i], 1);
+    bars->abort = 0;
+    mbar_fence_init();
+  } else if (warp == kWarpX && lane == 0) {
+    prefetch_tensormap(&tm_x);
+  } else if (warp == kWarpMma) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kWarpEpi) {
+    if (!p.early) griddep_wait();
+    int base = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int a = 0, b = 0;
+      if (e < p.E) {
+        a = p.offsets ? p.offsets[e] : 0;
+        b = p.offsets ? p.offsets[e + 1] : p.n_rows;
+      }
+      // offsets that leave [0, n_rows] or fall: nothing is computed
+      bad |= a < 0 || b < a || b > p.n_rows;
+      const int cnt = bad ? 0 : b - a;
+      const int n_nt = (cnt + p.cap - 1) / p.cap;
+      const int ntile = n_nt ? ((cnt + n_nt - 1) / n_nt + 15) / 16 * 16 : 16;
+      const int units = n_nt * p.n_mt * p.KB;
+      int incl = units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (e < p.E) {
+        SchedEntry en;
+        en.unit0 = base + incl - units;
+        en.start = a;
+        en.count = cnt;
+        en.n_nt = (n_nt << 16) | ntile;
+        sched[e] = en;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane == 0) {
+      if (bad) record_status(p.status, UW_ERR_INVALID_ARG);
+      sched[p.E].unit0 = bad ? 0 : base;
+      bars->total = bad ? 0 : base;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const int total = static_cast<int>(bars->total);
+  // with fewer units than CTAs the last CTAs have none: every CTA that the
+  // shares count has at least one
+  const int grid = min(p.grid, total);
+  const int cta = static_cast<int>(blockIdx.x);
+  const int u0 = cta < grid ? units_before(cta, total, grid) : 0;
+  const int u1 = cta < grid ? units_before(cta + 1, total, grid) : 0;
+  auto desc = [&](int m, int e) -> const ExpertDesc* { return p.table[m] ? p.table[m] + e : &p.one; };
+
+  if (warp == kWarpW) {
+    // --------------------------- weight producer ----------------------------
+    // Lanes hold the verbatim offsets of the next 31 tiles; lane 0 issues a
+    // tile's record and its verbatim rows (one contiguous run).
+    if (u0 < u1) {
+      const uint64_t once = l2_evict_first();
+      Seg s;
+      seg_init(s, sched, p, u0, u1);
+      Ring rw{0, 0};
+      int issued = 0;
+      bool ok = true;
+      do {
+        const uint8_t *pack[NMAT] = {}, *tails[NMAT] = {};
+        const uint32_t* off[NMAT] = {};
+        uint32_t n_verb[NMAT] = {}, v[NMAT] = {};
+        const int64_t t0 = static_cast<int64_t>(s.mt) * p.KB;
+        // lane l: offset of tile kb + l
+        auto fetch = [&](int m, int kb) -> uint32_t {
+          return kb + lane <= s.kb1 ? __ldg(off[m] + t0 + kb + lane) : 0u;
+        };
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m) {
+          const ExpertDesc* d = desc(m, s.e);
+          pack[m] = d->pack;
+          tails[m] = d->tails;
+          off[m] = d->pack_off;
+          n_verb[m] = d->n_verbatim;
+          v[m] = fetch(m, s.kb0);
+        }
+        // weights that a later column tile reads again stay in L2
+        const bool reread = (sched[s.e].n_nt >> 16) > 1;
+        for (int kb = s.kb0; kb < s.kb1 && ok; kb += 31) {
+          uint32_t nv[NMAT];
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) nv[m] = fetch(m, kb + 31);
+          const int n = min(31, s.kb1 - kb);
+          for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m) {
+              const uint32_t a = __shfl_sync(0xFFFFFFFFu, v[m], j), b = __shfl_sync(0xFFFFFFFFu, v[m], j + 1);
+              if (ok && rw.use > 0) ok = warp_wait(&bars->wempty[rw.slot], (rw.use - 1) & 1, bars, p.status);
+              if (!ok) continue;
+              if (lane == 0) {
+                uint32_t rows = 0;
+                if (b < a || b - a > 128u || b > n_verb[m]) record_status(p.status, UW_ERR_CORRUPT);
+                else rows = min(b - a, static_cast<uint32_t>(p.vcap));
+                uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
+                uint64_t* bar = &bars->wfull[rw.slot];
+                bars->tail_first[rw.slot] = a;
+                mbar_arrive_expect_tx(bar, kBody + rows * 128u);
+                const uint8_t* src = pack[m] + static_cast<uint64_t>(t0 + kb + j) * kBody;
+                if (reread) bulk_load(slot, src, kBody, bar);
+                else bulk_load_hint(slot, src, kBody, bar, once);
+                if (rows) bulk_load(slot + kBody, tails[m] + static_cast<uint64_t>(a) * 128u, rows * 128u, bar);
+              }
+              ++issued;
+              ring_next(rw, p.sw);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) v[m] = nv[m];
+        }
+      } while (ok && seg_next(s, sched, p));
+      // every issued copy lands before the CTA exits (already so unless a
+      // wait gave up)
+      if (lane == 0)
+        for (int q = max(0, issued - p.sw); q < issued; ++q)
+          mbar_wait(&bars->wfull[q % p.sw], static_cast<uint32_t>(q / p.sw) & 1, nullptr, p.status);
+    }
+    __syncwarp();
+  } else if (warp == kWarpX) {
+    // ------------------------- activation producer --------------------------
+    if (u0 < u1) {
+      griddep_wait();
+      Seg s;
+      seg_init(s, sched, p, u0, u1);
+      Ring rx{0, 0};
+      int issued = 0;
+      bool ok = true;
+      do {
+        // lane l gathers rows 4 l .. 4 l + 3 of the tile, and 4 (l + 32) ..
+        // past the tile's last row the last one again (never stored)
+        int r[2][4];
+        const int quads = s.ntile >> 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = s.slot0 + min(4 * (lane + 32 * h) + q, s.nvalid - 1);
+            int row = p.rows ? __ldg(p.rows + i) : i;
+            if (row < 0 || row >= p.x_rows) {
+              record_status(p.status, UW_ERR_INVALID_ARG);
+              row = 0;
+            }
+            r[h][q] = row;
+          }
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
+          if (rx.use > 0) ok = warp_wait(&bars->xempty[rx.slot], (rx.use - 1) & 1, bars, p.status);
+          if (!ok) break;
+          uint64_t* bar = &bars->xfull[rx.slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(s.ntile) * 128u);
+          __syncwarp();
+          uint8_t* dst = smem + static_cast<uint32_t>(rx.slot) * p.x_slot_bytes;
+          if (lane < quads) tma_gather4(dst + lane * 512, &tm_x, kb * 64, r[0][0], r[0][1], r[0][2], r[0][3], bar);
+          if (lane + 32 < quads)
+            tma_gather4(dst + (lane + 32) * 512, &tm_x, kb * 64, r[1][0], r[1][1], r[1][2], r[1][3], bar);
+          ++issued;
+          ring_next(rx, p.sx);
+        }
+      } while (ok && seg_next(s, sched, p));
+      if (lane == 0)
+        for (int q = max(0, issued - p.sx); q < issued; ++q)
+          mbar_wait(&bars->xfull[q % p.sx], static_cast<uint32_t>(q / p.sx) & 1, nullptr, p.status);
+    }
+    __syncwarp();
+  } else if (warp < kWarpRebuild) {
+    // ----------------------------- MMA issuers ------------------------------
+    // Tile i of the CTA's sequence belongs to issuer i % n_iss, which sums
+    // into an accumulator of its own (one thread issues an MMA only every
+    // ~120 cycles, several overlap).  Ring sizes are multiples of what keeps
+    // a slot with one issuer, so each sees every phase of its slots.
+    const int iss = warp - kWarpMma;
+    if (lane == 0 && iss < p.n_iss && u0 < u1) {
+      Seg s;
+      seg_init(s, sched, p, u0, u1);
+      Ring rx{0, 0}, ra{0, 0};
+      int turn = 0;
+      uint32_t ab = 0, seg = 0;
+      bool ok = true;
+      const uint64_t x_desc0 = smem_desc_sw128(smem_s);
+      do {
+        if (seg >= static_cast<uint32_t>(p.n_acc)) {
+          ok = mbar_wait(&bars->acc_empty[ab], (seg / p.n_acc - 1) & 1, &bars->abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t idesc = idesc_bf16_f32(s.ntile);
+        const uint32_t d = tmem + (ab * p.n_iss + iss) * static_cast<uint32_t>(p.cap);
+        uint32_t acc = 0;
+        for (int kb = s.kb0; kb < s.kb1 && ok; ++kb, ring_next(rx, p.sx)) {
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) {
+            if (ok && turn == iss) {
+              ok = mbar_wait(&bars->xfull[rx.slot], rx.use & 1, &bars->abort, p.status) &&
+                   mbar_wait(&bars->afull[ra.slot], ra.use & 1, &bars->abort, p.status);
+              if (ok) {
+                tc_fence_after();
+                const uint32_t a = tmem + p.a_col0 + static_cast<uint32_t>(ra.slot) * 32;
+                const uint64_t b = x_desc0 + static_cast<uint64_t>(static_cast<uint32_t>(rx.slot) * (p.x_slot_bytes >> 4));
+                mma_ts(d, a, b, idesc, acc);
+                mma_ts(d, a + 8, b + 2, idesc, 1u);
+                mma_ts(d, a + 16, b + 4, idesc, 1u);
+                mma_ts(d, a + 24, b + 6, idesc, 1u);
+                acc = 1;
+                tc_commit(&bars->aempty[ra.slot]);
+                tc_commit(&bars->xempty[rx.slot]);
+              }
+            }
+            if (++turn == p.n_iss) turn = 0;
+            ring_next(ra, p.sa);
+          }
+        }
+        if (!ok) break;
+        tc_commit(&bars->acc_full[ab]);
+        ++seg;
+        if (++ab == static_cast<uint32_t>(p.n_acc)) ab = 0;
+      } while (seg_next(s, sched, p));
+      // every MMA issued so far finishes before tensor memory is freed
+      tc_commit(&bars->drain[iss]);
+      mbar_wait(&bars->drain[iss], 0, nullptr, p.status);
+    }
+    __syncwarp();
+  } else if (warp < kWarpEpi) {
+    // ------------------------------- rebuild --------------------------------
+    // a warp reaches the TMEM lanes 32 (warp % 4) .., so those are its rows
+    const int r = (warp & 3) * 32 + lane;
+    const int grp = (warp - kWarpRebuild) >> 2;
+    if (u0 < u1) {
+      Seg s;
+      seg_init(s, sched, p, u0, u1);
+      Ring rw{0, 0}, ra{0, 0};
+      int turn = 0;
+      bool ok = true;
+      PaletteTables pal{};
+      bool uniform = true;
+      const uint8_t* tails = nullptr;
+      uint32_t n_verb = 0;
+      int cur_e = -1;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>((r >> 5) * 32) << 16) + p.a_col0;
+      do {
+        for (int kb = s.kb0; kb < s.kb1 && ok; ++kb) {
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) {
+            if (ok && turn == grp) {
+              if (cur_e != s.e) {  // with two matrices, a group always has the same one
+                const ExpertDesc* d = desc(m, s.e);
+                pal = load_palette(d);
+                uniform = d->mixed == 0;
+                tails = d->tails;
+                n_verb = d->n_verbatim;
+                cur_e = s.e;
+              }
+              ok = warp_wait(&bars->wfull[rw.slot], rw.use & 1, bars, p.status);
+              if (ok) {
+                const uint32_t body = smem_s + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
+                uint32_t o[32];
+                if (uniform) rebuild_row(pal, true, body, r, o);
+                else rebuild_row(pal, false, body, r, o);
+                // verbatim rows: one mask bit per row, no per-element test
+                const uint4 mk = lds128(body + kBodyMask);
+                const int w = r >> 5;
+                const uint32_t mw = w == 0 ? mk.x : (w == 1 ? mk.y : (w == 2 ? mk.z : mk.w));
+                if ((mw >> lane) & 1) {
+                  const int idx = (w > 0 ? __popc(mk.x) : 0) + (w > 1 ? __popc(mk.y) : 0) +
+                                  (w > 2 ? __popc(mk.z) : 0) + __popc(mw & ((1u << lane) - 1));
+                  if (idx < p.vcap) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                      const uint4 v = lds128(body + kBody + idx * 128 + 16 * c);
+                      o[4 * c] = v.x;
+                      o[4 * c + 1] = v.y;
+                      o[4 * c + 2] = v.z;
+                      o[4 * c + 3] = v.w;
+                    }
+                  } else {
+                    // more verbatim rows than staged ones: from HBM
+                    const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
+                    if (g < n_verb) {
+                      const uint4* src = reinterpret_cast<const uint4*>(tails + g * 128u);
+#pragma unroll
+                      for (int c = 0; c < 8; ++c) {
+                        const uint4 v = __ldg(src + c);
+                        o[4 * c] = v.x;
+                        o[4 * c + 1] = v.y;
+                        o[4 * c + 2] = v.z;
+                        o[4 * c + 3] = v.w;
+                      }
+                    } else {
+                      record_status(p.status, UW_ERR_CORRUPT);
+                    }
+                  }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->wempty[rw.slot]);
+                // the A slot is free once the MMAs of its previous use are done
+                if (ra.use > 0) ok = warp_wait(&bars->aempty[ra.slot], (ra.use - 1) & 1, bars, p.status);
+                if (ok) {
+                  tc_fence_after();
+                  tmem_st32(lanes + static_cast<uint32_t>(ra.slot) * 32, o);
+                  tc_wait_st();
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&bars->afull[ra.slot]);
+                }
+              }
+            }
+            if (++turn == kGroups) turn = 0;
+            ring_next(rw, p.sw);
+            ring_next(ra, p.sa);
+          }
+        }
+      } while (ok && seg_next(s, sched, p));
+    }
+  } else {
+    // ------------------------------- epilogue -------------------------------
+    // outputs and the workspace may be in use by the previous kernel on the
+    // stream until it has completed
+    griddep_wait();
+    if (warp == kWarpEpi && lane == 0) griddep_launch_dependents();
+    if (u0 < u1) {
+      const int w = warp & 3;  // TMEM lanes 32 w ..
+      const int r = w * 32 + lane;
+      const bool elected = warp == kWarpEpi && lane == 0;
+      volatile uint32_t* last_flag = &bars->last_arriver;
+      Seg s;
+      seg_init(s, sched, p, u0, u1);
+      uint32_t seg = 0;
+      int first_tile = 0;  // the segment's first tile in the CTA's sequence
+      const int per = p.n_iss / NMAT;  // issuers per matrix
+      do {
+        const uint32_t ab = seg % p.n_acc;
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[ab], (seg / p.n_acc) & 1, &bars->abort, p.status));
+        if (!group_and(ok)) break;
+        tc_fence_after();
+        const int n = s.mt * 128 + r;
+        const int n_kb = s.kb1 - s.kb0;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap);
+        const int n_chunks = (s.nvalid + 15) >> 4;
+        // this CTA's sums of 16 columns of matrix m: its issuers' sums in
+        // the order of their first k-block (a segment shorter than the
+        // number of issuers leaves some without)
+        auto own_sum = [&](int m, int cc, float (&acc)[16]) {
+#pragma unroll 1
+          for (int i = 0; i < per && i < n_kb; ++i) {
+            const int issuer = (first_tile + i * NMAT + m) % p.n_iss;
+            uint32_t v[16];
+            tmem_ld16(taddr + static_cast<uint32_t>(issuer * p.cap + cc * 16), v);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[j] = i ? acc[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+          }
+        };
+        const bool row_ok = n < p.N;
+        const float bias = p.bias && row_ok ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
+                                                  p.bias)[static_cast<int64_t>(s.e) * p.N + n])
+                                            : 0.0f;
+        auto emit = [&](const float (&a)[NMAT][16], int cc) {
+          if (!row_ok) return;
+          const int cols = min(16, s.nvalid - cc * 16);
+          int64_t i = static_cast<int64_t>(s.slot0 + cc * 16) * p.N + n;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, i += p.N) {
+            if (j >= cols) continue;
+            float v = a[0][j];
+            if constexpr (NMAT == 2) {
+              v = v / (1.0f + expf(-v)) * a[1][j];
+            } else {
+              if (p.bias) v += bias;
+              v = activate(v, p.act);
+              if (p.residual) v += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
+            }
+            if (p.out_fp32) static_cast<float*>(p.y)[i] = v;
+            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
+          }
+        };
+        if (n_kb == p.KB) {
+          for (int cc = 0; cc < n_chunks; ++cc) {
+            float a[NMAT][16];
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m) own_sum(m, cc, a[m]);
+            emit(a, cc);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
+        } else {
+          // part of a tile: contributors c_first..c_last
+          const int c_first = unit_owner(s.tile_u, total, grid);
+          const int c_last = unit_owner(s.tile_u + p.KB - 1, total, grid);
+          const int n_contrib = c_last - c_first + 1;
+          // contributor c's sums: its slot 0 when the tile opens its share,
+          // else slot 1; [matrix][chunk][weight row][16 columns]
+          auto part = [&](int c) -> float* {
+            const int which = units_before(c, total, grid) >= s.tile_u ? 0 : 1;
+            return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
+          };
+          float* mine = part(cta);
+          for (int cc = 0; cc < n_chunks; ++cc) {
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m) {
+              float a[16];
+              own_sum(m, cc, a);
+              float4* dst = reinterpret_cast<float4*>(mine + ((m * n_chunks + cc) * 128 + r) * 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) __stcg(dst + k, make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
+          group_sync();  // every store of the group precedes the ticket
+          if (elected) {
+            // a CTA opens at most one tile that others finish: its counter
+            const bool last = atom_add_acq_rel_gpu(p.counters + c_first, 1u) == static_cast<uint32_t>(n_contrib - 1);
+            if (last) p.counters[c_first] = 0;  // all have arrived: ready for the next launch
+            *last_flag = last ? 1u : 0u;
+          }
+          group_sync();
+          if (*last_flag) {
+            for (int cc = 0; cc < n_chunks; ++cc) {
+              float a[NMAT][16];
+#pragma unroll
+              for (int m = 0; m < NMAT; ++m) {
+                const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 16;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) a[m][j] = 0.0f;
+#pragma unroll 2
+                for (int c = c_first; c <= c_last; ++c) {
+                  const float4* src = reinterpret_cast<const float4*>(part(c) + at);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float4 v = __ldcg(src + k);
+                    a[m][4 * k] += v.x;
+                    a[m][4 * k + 1] += v.y;
+                    a[m][4 * k + 2] += v.z;
+                    a[m][4 * k + 3] += v.w;
+                  }
+                }
+              }
+              emit(a, cc);
+            }
+          }
+          group_sync();  // the flag word is used again by the next such tile
+        }
+        ++seg;
+        first_tile += n_kb * NMAT;
+      } while (seg_next(s, sched, p));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------- host side -----------------------------------
+
+struct GLayout {
+  int cap = 16, n_iss = 1, n_acc = 1, sx = 2, sa = 2, sw = 2, vcap = 0;
+  uint32_t x_slot_bytes = 0, w_base = 0, w_slot_bytes = 0, sched_off = 0, bar_off = 0, a_col0 = 0;
+  size_t smem = 0;
+};
+
+int env_int(const char* name, int dflt) {
+  const char* e = std::getenv(name);
+  return e ? std::atoi(e) : dflt;
+}
+
+// Columns per tile: what an average group needs, with room for uneven ones.
+int pick_cap(int n_rows, int E, int nmat) {
+  const int most = nmat == 2 ? 192 : 256;
+  static int forced = env_int("UW_GROUPED_CAP", 0);
+  if (forced) return std::min(forced, most);
+  int64_t want = n_rows;
+  if (E > 1) want = std::min<int64_t>(n_rows, 4 * ((static_cast<int64_t>(n_rows) + E - 1) / E));
+  const int64_t tiles = (want + most - 1) / most;
+  want = (want + tiles - 1) / tiles;
+  return static_cast<int>(std::max<int64_t>(16, (want + 15) / 16 * 16));
+}
+
+bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
+  GLayout l;
+  l.cap = pick_cap(n_rows, E, nmat);
+  // tensor memory: accumulators (n_acc buffers x n_iss issuers x cap
+  // columns), then 32 columns per A tile
+  l.n_acc = 2 * nmat * l.cap <= 256 ? 2 : 1;
+  l.n_iss = nmat;
+  while (2 * l.n_iss <= kMaxIssuers && l.n_acc * 2 * l.n_iss * l.cap <= 256) l.n_iss *= 2;
+  l.a_col0 = (static_cast<uint32_t>(l.n_acc * l.n_iss * l.cap) + 31u) & ~31u;
+  const int per = l.n_iss / nmat;            // issuers per matrix: an x slot stays with one of them
+  const int step_a = std::max(l.n_iss, kGroups);
+  l.sa = std::min(kMaxSlots, static_cast<int>((kTmemCols - l.a_col0) / 32));
+  l.sa -= l.sa % step_a;
+  l.x_slot_bytes = static_cast<uint32_t>(l.cap) * 128;
+  const uint32_t sched_bytes = (static_cast<uint32_t>(E + 1) * sizeof(SchedEntry) + 127u) & ~127u;
+  const uint32_t fixed = sched_bytes + ((sizeof(GBars) + 127u) & ~127u) + 128u + 1024u;
+  if (l.sa < step_a || fixed >= kSmemLimit / 2) return false;
+  const uint32_t room = static_cast<uint32_t>(kSmemLimit) - fixed;
+  l.sx = l.cap <= 32 ? 8 : (l.cap <= 64 ? 6 : (l.cap <= 128 ? 4 : 3));
+  l.sx -= l.sx % per;
+  const uint32_t w_room = room - static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
+  l.sw = std::min(kMaxSlots, static_cast<int>(w_room / (kBody + kMinTail * 128u)));
+  l.sw -= l.sw % kGroups;
+  if (l.sw < kGroups || l.sx < 1) return false;
+  l.vcap = static_cast<int>(std::min(128u, (w_room / static_cast<uint32_t>(l.sw) - kBody) / 128u));
+  l.w_slot_bytes = kBody + static_cast<uint32_t>(l.vcap) * 128u;  // a multiple of 16
+  l.w_base = static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
+  l.sched_off = (l.w_base + static_cast<uint32_t>(l.sw) * l.w_slot_bytes + 127u) & ~127u;
+  l.bar_off = l.sched_off + sched_bytes;
+  l.smem = std::max<size_t>(l.bar_off + ((sizeof(GBars) + 127u) & ~127u) + 1024u, kSmemFloor);
+  if (l.smem > kSmemLimit) return false;
+  *out = l;
+  return true;
+}
+
+struct GPlan {
+  GLayout lay;
+  int n_mt = 0, KB = 0, grid = 0;
+  size_t partial_stride = 0;  // floats
+  size_t bytes = 0;           // workspace
+};
+
+uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, int sms, GPlan* out) {
+  if (E < 1 || E > kMaxExperts || n_rows < 0) return UW_ERR_INVALID_ARG;
+  if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
+  GPlan g;
+  if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
+  g.n_mt = static_cast<int>((N + 127) / 128);
+  g.KB = static_cast<int>(K / 64);
+  // the most units any split of n_rows into E groups can give
+  const int64_t tiles = std::min<int64_t>(n_rows, n_rows / g.lay.cap + E);
+  const int64_t units = tiles * g.n_mt * g.KB;
+  if (units > 0x7FFFFFFF || n_rows / g.lay.cap + 1 > 0x7FFF) return UW_ERR_UNSUPPORTED_SHAPE;
+  g.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), sms));
+  g.partial_stride = static_cast<size_t>(nmat) * 128 * g.lay.cap;
+  g.bytes = kWsHeader + kCounterBytes + align_up(2 * static_cast<size_t>(g.grid) * g.partial_stride * 4, 256);
+  *out = g;
+  return UW_OK;
+}
+
+template <int NMAT>
+uw_status launch_grouped_kernel(const CUtensorMap& tx, const GParams& gp, size_t smem, cudaStream_t s) {
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(once[dev & 63], [&] {
+    attr_err[dev & 63] = cudaFuncSetAttribute(grouped_kernel<NMAT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(kSmemLimit));
+  });
+  if (attr_err[dev & 63] != cudaSuccess) return UW_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(gp.grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_kernel<NMAT>, tx, gp);
+  note_launch();
+  if (err != cudaSuccess) return cuda_status(err);
+  return cuda_status(cudaGetLastError());
+}
+
+int sms_or_default() {
+  DeviceInfo dev;
+  return device_info(&dev) == UW_OK ? dev.sm_count : 148;
+}
+
+}  // namespace
+
+// The device record of one compressed matrix (direct-palette form).
+uw_status expert_desc(const uw_matrix* m, ExpertDesc* out) {
+  uw_status st = check_matrix(m);
+  if (st != UW_OK) return st;
+  if (!m->pack || !m->pack_off || !aligned16(m->pack) || !aligned16(m->pack_off)) return UW_ERR_INVALID_ARG;
+  const int64_t n_tiles = (m->L.rows + 127) / 128 * (m->L.cols / 64);
+  if (m->L.n_verbatim > 0xFFFFFFFFll) return UW_ERR_UNSUPPORTED_SHAPE;
+  bool mixed = false;
+  const PaletteTables t = palette_tables(m->cb.palette, m->cb.code_len, &mixed);
+  ExpertDesc d;
+  std::memset(&d, 0, sizeof(d));
+  d.pack = m->pack;
+  d.tails = m->pack + static_cast<uint64_t>(n_tiles) * kBody;
+  d.pack_off = m->pack_off;
+  d.n_verbatim = static_cast<uint32_t>(m->L.n_verbatim);
+  d.mixed = mixed ? 1 : 0;
+  d.lo0 = t.lo0;
+  d.lo1 = t.lo1;
+  d.hi0 = t.hi0;
+  d.hi1 = t.hi1;
+  d.b7lo0 = t.b7lo0;
+  d.b7lo1 = t.b7lo1;
+  d.b7hi0 = t.b7hi0;
+  d.b7hi1 = t.b7hi1;
+  d.keep = t.keep;
+  *out = d;
+  return UW_OK;
+}
+
+size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat) {
+  GPlan g;
+  return grouped_plan(N, K, E, n_rows, nmat, sms_or_default(), &g) == UW_OK ? g.bytes : 0;
+}
+
+uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
+  DeviceInfo dev;
+  uw_status st = device_info(&dev);
+  if (st != UW_OK) return st;
+  const int nmat = a.swiglu ? 2 : 1;
+  GPlan g;
+  if ((st = grouped_plan(a.N, a.K, a.E, a.n_rows, nmat, dev.sm_count, &g)) != UW_OK) return st;
+  if (!a.x || !a.y || !a.ws || !aligned16(a.x) || !aligned16(a.y) || !aligned16(a.ws) || a.x_rows < 1)
+    return UW_ERR_INVALID_ARG;
+  if (!aligned_to(a.offsets, 4) || !aligned_to(a.rows, 4) || !aligned_to(a.bias, 2) || !aligned_to(a.residual, 2))
+    return UW_ERR_INVALID_ARG;
+  if (a.activation < UW_ACT_NONE || a.activation > UW_ACT_SILU || a.out_type < UW_OUT_BF16 ||
+      a.out_type > UW_OUT_FP32)
+    return UW_ERR_INVALID_ARG;
+  if (a.ws_bytes < g.bytes) return UW_ERR_WORKSPACE_TOO_SMALL;
+  CUtensorMap tx;
+  if ((st = make_tensor_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, static_cast<uint64_t>(a.K),
+                               static_cast<uint64_t>(a.x_rows), static_cast<uint64_t>(a.K) * 2, 64, 1,
+                               CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
+    return st;
+  GParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.E = a.E;
+  p.N = static_cast<int>(a.N);
+  p.KB = g.KB;
+  p.n_mt = g.n_mt;
+  p.x_rows = a.x_rows;
+  p.n_rows = a.n_rows;
+  p.grid = g.grid;
+  p.cap = g.lay.cap;
+  p.n_iss = g.lay.n_iss;
+  p.n_acc = g.lay.n_acc;
+  p.sx = g.lay.sx;
+  p.sa = g.lay.sa;
+  p.sw = g.lay.sw;
+  p.x_slot_bytes = g.lay.x_slot_bytes;
+  p.w_base = g.lay.w_base;
+  p.w_slot_bytes = g.lay.w_slot_bytes;
+  p.sched_off = g.lay.sched_off;
+  p.bar_off = g.lay.bar_off;
+  p.a_col0 = g.lay.a_col0;
+  p.vcap = g.lay.vcap;
+  p.early = a.offsets == nullptr || a.offsets_ready;
+  p.offsets = a.offsets;
+  p.rows = a.rows;
+  p.table[0] = static_cast<const ExpertDesc*>(a.table[0]);
+  p.table[1] = static_cast<const ExpertDesc*>(a.table[1]);
+  if (a.one) p.one = *a.one;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.act = a.activation;
+  p.out_fp32 = a.out_type == UW_OUT_FP32;
+  p.y = a.y;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  p.counters = reinterpret_cast<uint32_t*>(ws + kWsHeader);
+  p.partials = reinterpret_cast<float*>(ws + kWsHeader + kCounterBytes);
+  p.partial_stride = static_cast<long long>(g.partial_stride);
+  return nmat == 2 ? launch_grouped_kernel<2>(tx, p, g.lay.smem, s) : launch_grouped_kernel<1>(tx, p, g.lay.smem, s);
+}
+
+}  // namespace uw
+
+using namespace uw;
+
+extern "C" size_t uw_experts_table_bytes(int32_t n_experts) {
+  return n_experts < 1 || n_experts > kMaxExperts ? 0 : static_cast<size_t>(n_experts) * sizeof(ExpertDesc);
+}
+
+extern "C" uw_status uw_experts_init(const uw_matrix* const* mats, int32_t n_experts, void* table, size_t table_bytes,
+                                     uw_experts* out, void* stream) {
+  if (!mats || !table || !out || n_experts < 1 || n_experts > kMaxExperts || !aligned16(table)) return UW_ERR_INVALID_ARG;
+  if (table_bytes < uw_experts_table_bytes(n_experts)) return UW_ERR_WORKSPACE_TOO_SMALL;
+  std::vector<ExpertDesc> host(static_cast<size_t>(n_experts));
+  for (int32_t e = 0; e < n_experts; ++e) {
+    if (!mats[e]) return UW_ERR_INVALID_ARG;
+    if (mats[e]->L.rows != mats[0]->L.rows || mats[e]->L.cols != mats[0]->L.cols) return UW_ERR_UNSUPPORTED_SHAPE;
+    const uw_status st = expert_desc(mats[e], &host[static_cast<size_t>(e)]);
+    if (st != UW_OK) return st;
+  }
+  DeviceInfo dev;
+  uw_status st = device_info(&dev);
+  if (st != UW_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(table, host.data(), host.size() * sizeof(ExpertDesc), cudaMemcpyHostToDevice, s) != cudaSuccess)
+    return UW_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return UW_ERR_CUDA;  // the host copy goes away
+  std::memset(out, 0, sizeof(*out));
+  out->n_experts = n_experts;
+  out->rows = mats[0]->L.rows;
+  out->cols = mats[0]->L.cols;
+  out->table = table;
+  return UW_OK;
+}
+
+namespace {
+bool experts_ok(const uw_experts* w) { return w && w->table && aligned16(w->table); }
+}  // namespace
+
+extern "C" size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, int32_t swiglu) {
+  return w ? grouped_ws_bytes(w->rows, w->cols, w->n_experts, n_rows, swiglu ? 2 : 1) : 0;
+}
+
+extern "C" uw_status uw_gemm_grouped(const uw_experts* w, const uint16_t* x, int32_t x_rows, const int32_t* rows,
+                                     const int32_t* offsets, int32_t n_rows, const uw_epilogue* epi, void* y,
+                                     void* ws, size_t ws_bytes, void* stream) {
+  if (!experts_ok(w) || !offsets || n_rows < 0 || x_rows < 0) return UW_ERR_INVALID_ARG;
+  if (!rows && x_rows < n_rows) return UW_ERR_INVALID_ARG;  // row s of x is slot s
+  if (n_rows == 0) return UW_OK;
+  GroupedArgs a;
+  a.N = w->rows;
+  a.K = w->cols;
+  a.E = w->n_experts;
+  a.table[0] = w->table;
+  a.x = x;
+  a.x_rows = x_rows;
+  a.rows = rows;
+  a.offsets = offsets;
+  a.n_rows = n_rows;
+  if (epi) {
+    a.bias = epi->bias;
+    a.residual = epi->residual;
+    a.activation = epi->activation;
+    a.out_type = epi->out_type;
+  }
+  a.y = y;
+  a.ws = ws;
+  a.ws_bytes = ws_bytes;
+  return launch_grouped(a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" uw_status uw_gemm_grouped_swiglu(const uw_experts* gate, const uw_experts* up, const uint16_t* x,
+                                            int32_t x_rows, const int32_t* rows, const int32_t* offsets,
+                                            int32_t n_rows, uint16_t* h, void* ws, size_t ws_bytes, void* stream) {
+  if (!experts_ok(gate) || !experts_ok(up) || !offsets || n_rows < 0 || x_rows < 0) return UW_ERR_INVALID_ARG;
+  if (gate->n_experts != up->n_experts || gate->rows != up->rows || gate->cols != up->cols) return UW_ERR_INVALID_ARG;
+  if (!rows && x_rows < n_rows) return UW_ERR_INVALID_ARG;
+  if (n_rows == 0) return UW_OK;
+  GroupedArgs a;
+  a.N = gate->rows;
+  a.K = gate->cols;
+  a.E = gate->n_experts;
+  a.swiglu = true;
+  a.table[0] = gate->table;
+  a.table[1] = up->table;
+  a.x = x;
+  a.x_rows = x_rows;
+  a.rows = rows;
+  a.offsets = offsets;
+  a.n_rows = n_rows;
+  a.y = h;
+  a.ws = ws;
+  a.ws_bytes = ws_bytes;
+  return launch_grouped(a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t uw_gemm_epilogue_workspace_bytes(const uw_layout* L, int32_t batch) {
+  return L ? grouped_ws_bytes(L->rows, L->cols, 1, batch, 1) : 0;
+}
+
+extern "C" uw_status uw_gemm_epilogue(const uw_matrix* m, const uint16_t* x, int32_t batch, const uw_epilogue* epi,
+                                      void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!m || batch < 0) return UW_ERR_INVALID_ARG;
+  ExpertDesc d;
+  const uw_status st = expert_desc(m, &d);
+  if (st != UW_OK) return st;
+  if (batch == 0) return UW_OK;
+  GroupedArgs a;
+  a.N = m->L.rows;
+  a.K = m->L.cols;
+  a.E = 1;
+  a.one = &d;
+  a.x = x;
+  a.x_rows = batch;
+  a.n_rows = batch;
+  if (epi) {
+    a.bias = epi->bias;
+    a.residual = epi->residual;
+    a.activation = epi->activation;
+    a.out_type = epi->out_type;
+  }
+  a.y = y;
+  a.ws = ws;
+  a.ws_bytes = ws_bytes;
+  return launch_grouped(a, static_cast<cudaStream_t>(stream));
+}

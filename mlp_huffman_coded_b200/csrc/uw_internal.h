@@ -67,6 +67,7 @@ size_t pipeline_scratch_bytes(const uw_layout* L, int pipeline);
 
 // Device pointer checks.
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 uw_status check_matrix(const uw_matrix* m);
 
 // Kernel launchers (asynchronous).
@@ -104,5 +105,44 @@ struct GemmArgs {
 };
 uw_status launch_gemm(const GemmArgs& a, cudaStream_t s);
 uw_status launch_swiglu(const uint16_t* g, const uint16_t* u, uint16_t* h, int64_t n, cudaStream_t s);
+
+
+// Products grouped by expert.  The device record of one compressed matrix:
+// where its pack lies and its palette tables (PaletteTables).
+constexpr int kMaxExperts = UW_MAX_EXPERTS;
+struct alignas(16) ExpertDesc {
+  const uint8_t* pack;       // tile records
+  const uint8_t* tails;      // verbatim rows, tile order
+  const uint32_t* pack_off;  // per tile: verbatim rows of all earlier tiles
+  uint32_t n_verbatim, mixed;
+  uint32_t lo0, lo1, hi0, hi1, b7lo0, b7lo1, b7hi0, b7hi1, keep;
+  uint32_t reserved[3];
+};
+static_assert(sizeof(ExpertDesc) == 80, "uw_experts_table_bytes");
+uw_status expert_desc(const uw_matrix* m, ExpertDesc* out);
+
+struct GroupedArgs {
+  int64_t N = 0, K = 0;
+  int E = 1;
+  bool swiglu = false;                         // table[0] = gate, table[1] = up
+  const void* table[2] = {nullptr, nullptr};   // device ExpertDesc[E]; NULL: `one` is the only group's
+  const ExpertDesc* one = nullptr;             // host
+  const uint16_t* x = nullptr;
+  int x_rows = 0;
+  const int32_t* rows = nullptr;     // row of x per slot, NULL: slot s reads row s
+  const int32_t* offsets = nullptr;  // first slot of each group, NULL: one group of n_rows
+  // The offsets were written before the kernel just ahead on the stream
+  // started: they are read, and weights stream, before waiting for it.
+  bool offsets_ready = false;
+  int n_rows = 0;
+  const uint16_t* bias = nullptr;
+  const uint16_t* residual = nullptr;
+  int activation = UW_ACT_NONE, out_type = UW_OUT_BF16;
+  void* y = nullptr;
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+};
+size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat);  // 0: unsupported
+uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s);
 
 }  // namespace uw

@@ -1,0 +1,585 @@
+// Mixture-of-experts glue around the products grouped by expert: the router
+// (softmax, top-k, grouping of the tokens by expert), the weighted
+// combination of the experts' outputs, and the whole sparse MLP block.
+//
+// The Unweight page compresses the matrices of dense MLPs; a sparse MLP holds
+// the same three matrices once per expert.  The block is not on the page.
+#include <algorithm>
+#include <cfloat>
+#include <cstring>
+
+#include "uw_device.cuh"
+#include "uw_internal.h"
+
+namespace uw {
+
+namespace {
+
+// ------------------------------- router --------------------------------------
+// One warp per token, the token's logits in registers (EPL per lane: expert
+// lane + 32 i).  Each of the top_k steps finds the largest remaining logit
+// with one warp reduction and the lowest expert that has it with a second;
+// the tokens of a block that chose an expert are a bit mask in shared memory,
+// so a token's place among them is a population count, whatever the order of
+// the atomics.
+//
+// A prompt takes two launches: the first chooses and counts per block, the
+// second adds up the counts of the blocks before it (at most kMaxRouteBlocks)
+// and places the tokens.  Up to 64 tokens take one block and one launch.
+// Launch latency bounds both: 8192 tokens x 64 experts are 1 MB of BF16 logits.
+constexpr int kRouteWarps = 16, kRouteThreads = 32 * kRouteWarps;
+constexpr int kRouteChunk = 64;       // tokens ranked together (two mask words)
+constexpr int kMaxRouteBlocks = 128;  // a block ranks as many chunks as that needs
+
+struct RouteParams {
+  const void* logits;
+  int fp32, T, E, k, renormalize;
+  int tokens_per_block;
+  float* weights;
+  int32_t* experts;
+  int32_t* slots;
+  int32_t* rows;
+  int32_t* offsets;
+  int32_t* counts;  // [blocks][E]
+};
+
+// Ordered key of a logit: larger logit, larger key; 0 for one that can never
+// be chosen (-inf, NaN).  +inf counts as the largest finite value.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(fminf(v, FLT_MAX) + 0.0f);  // -0 becomes +0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
+template <int EPL>
+__device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, uint32_t* masks, uint32_t word,
+                                       uint32_t bit) {
+  uint32_t key[EPL];
+  const int64_t base = static_cast<int64_t>(t) * p.E;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
+    float v = -INFINITY;
+    if (e < p.E)
+      v = p.fp32 ? static_cast<const float*>(p.logits)[base + e]
+                 : __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[base + e]);
+    key[i] = logit_key(v);
+  }
+  uint32_t local = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) local = max(local, key[i]);
+  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, local);
+  const float vmax = key_logit(top);
+  float whole = 0.0f;  // sum of exp(l - max) over all experts
+  if (!p.renormalize && top) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) whole += key[i] ? expf(key_logit(key[i]) - vmax) : 0.0f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) whole += __shfl_xor_sync(0xFFFFFFFFu, whole, d);
+  }
+  float mine = 0.0f;  // lane j: the j-th choice
+  int chosen = -1;
+  uint32_t best = top;
+  for (int j = 0; j < p.k; ++j) {
+    if (j) {
+      local = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) local = max(local, key[i]);
+      best = __reduce_max_sync(0xFFFFFFFFu, local);
+    }
+    if (!best) break;
+    uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i)
+      if (key[i] == best) at = static_cast<uint32_t>(lane + 32 * i);
+    at = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (at == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+    const float e = expf(key_logit(best) - vmax);
+    if (p.renormalize) whole += e;
+    if (lane == j) {
+      mine = e;
+      chosen = static_cast<int>(at);
+    }
+  }
+  if (lane < p.k) {
+    const int64_t i = static_cast<int64_t>(t) * p.k + lane;
+    p.experts[i] = chosen;
+    p.weights[i] = chosen < 0 ? 0.0f : mine / whole;
+    if (chosen >= 0) atomicOr(&masks[2 * chosen + word], bit);
+  }
+}
+
+// Exclusive scan of total[0..E) into first[0..E]; one warp.
+__device__ __forceinline__ void scan_experts(const int32_t* total, int32_t* first, int E, int lane) {
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int v = e0 + lane < E ? total[e0 + lane] : 0;
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += u;
+    }
+    if (e0 + lane < E) first[e0 + lane] = base + incl - v;
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  if (lane == 0) first[E] = base;
+}
+
+// Slots of the tokens [t0, t0 + n) from their masks and each expert's next
+// free slot (advanced afterwards by the caller).
+__device__ __forceinline__ void place(const RouteParams& p, int t0, int n, const uint32_t* masks, const int32_t* next) {
+  for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
+    const int t = i / p.k;
+    const int64_t at = static_cast<int64_t>(t0) * p.k + i;
+    const int e = p.experts[at];
+    int slot = -1;
+    if (e >= 0) {
+      const uint32_t lo = masks[2 * e], hi = masks[2 * e + 1];
+      const int before = t < 32 ? __popc(lo & ((1u << t) - 1)) : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1));
+      slot = next[e] + before;
+      p.rows[slot] = t0 + t;
+    }
+    p.slots[at] = slot;
+  }
+}
+
+// Chooses the experts of a block's tokens.  ONE: the only block, which places
+// them too; else the block's counts go to the workspace.
+template <int EPL, bool ONE>
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
+  extern __shared__ int32_t sh[];
+  uint32_t* masks = reinterpret_cast<uint32_t*>(sh);  // [E][2]
+  int32_t* total = sh + 2 * p.E;                      // [E]
+  int32_t* first = total + p.E;                       // [E + 1]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+    masks[2 * e] = masks[2 * e + 1] = 0;
+    total[e] = 0;
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t0 = blockIdx.x * p.tokens_per_block, t1 = min(p.T, t0 + p.tokens_per_block);
+  __syncthreads();
+  for (int c = t0; c < t1; c += kRouteChunk) {
+    for (int t = c + warp; t < min(t1, c + kRouteChunk); t += kRouteWarps)
+      choose<EPL>(p, t, lane, masks, static_cast<uint32_t>((t - c) >> 5), 1u << ((t - c) & 31));
+    __syncthreads();
+    if constexpr (!ONE) {
+      for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+        total[e] += __popc(masks[2 * e]) + __popc(masks[2 * e + 1]);
+        masks[2 * e] = masks[2 * e + 1] = 0;
+      }
+      __syncthreads();
+    }
+  }
+  if constexpr (ONE) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) total[e] = __popc(masks[2 * e]) + __popc(masks[2 * e + 1]);
+    __syncthreads();
+    if (warp == 0) scan_experts(total, first, p.E, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+    place(p, 0, p.T, masks, first);
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = total[e];
+  }
+}
+
+__global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p) {
+  extern __shared__ int32_t sh[];
+  uint32_t* masks = reinterpret_cast<uint32_t*>(sh);  // [E][2]
+  int32_t* total = sh + 2 * p.E;                      // [E]
+  int32_t* first = total + p.E;                       // [E + 1]
+  int32_t* before = first + p.E + 1;                  // [E] choices of earlier blocks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+    masks[2 * e] = masks[2 * e + 1] = 0;
+    total[e] = before[e] = 0;
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  // several threads per expert, each a run of blocks; integer sums, so the
+  // order of the shared-memory atomics does not matter
+  const int parts = max(1, kRouteThreads / p.E);
+  for (int i = threadIdx.x; i < parts * p.E; i += kRouteThreads) {
+    const int e = i % p.E, part = i / p.E;
+    int all = 0, earlier = 0;
+#pragma unroll 8
+    for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
+      const int v = __ldcg(p.counts + static_cast<int64_t>(b) * p.E + e);
+      all += v;
+      if (b < static_cast<int>(blockIdx.x)) earlier += v;
+    }
+    atomicAdd(&total[e], all);
+    atomicAdd(&before[e], earlier);
+  }
+  __syncthreads();
+  if (warp == 0) scan_experts(total, first, p.E, lane);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) first[e] += before[e];
+  __syncthreads();
+  const int t0 = blockIdx.x * p.tokens_per_block, t1 = min(p.T, t0 + p.tokens_per_block);
+  for (int c = t0; c < t1; c += kRouteChunk) {
+    const int n = min(kRouteChunk, t1 - c);
+    for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
+      const int e = p.experts[static_cast<int64_t>(c) * p.k + i], t = i / p.k;
+      if (e >= 0) atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
+    }
+    __syncthreads();
+    place(p, c, n, masks, first);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+      first[e] += __popc(masks[2 * e]) + __popc(masks[2 * e + 1]);
+      masks[2 * e] = masks[2 * e + 1] = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// Launch with programmatic dependent launch: every kernel here waits for the
+// one ahead before it touches memory that one may use.
+template <typename... Args>
+uw_status launch_pdl(void (*kernel)(Args...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+  note_launch();
+  if (err != cudaSuccess) return cuda_status(err);
+  return cuda_status(cudaGetLastError());
+}
+
+struct RoutePlan {
+  int blocks = 1, tokens_per_block = kRouteChunk;
+  size_t bytes = 0;
+};
+bool route_plan(int64_t T, int64_t E, int64_t k, RoutePlan* out) {
+  if (T < 0 || T > UW_MAX_TOKENS || E < 1 || E > kMaxExperts || k < 1 || k > E || k > UW_MAX_TOP_K) return false;
+  RoutePlan r;
+  const int64_t chunks = std::max<int64_t>(1, (T + kRouteChunk - 1) / kRouteChunk);
+  const int64_t per = (chunks + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
+  r.tokens_per_block = static_cast<int>(per * kRouteChunk);
+  r.blocks = static_cast<int>((chunks + per - 1) / per);
+  r.bytes = kWsHeader + kCounterBytes + (r.blocks > 1 ? align_up(static_cast<size_t>(r.blocks) * E * 4, 256) : 0);
+  *out = r;
+  return true;
+}
+
+template <int EPL>
+uw_status launch_route_epl(const RouteParams& p, const RoutePlan& r, cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(4 * p.E + 1) * 4;
+  if (r.blocks == 1) return launch_pdl(route_kernel<EPL, true>, 1u, kRouteThreads, smem, s, p);
+  return launch_pdl(route_kernel<EPL, false>, static_cast<unsigned>(r.blocks), kRouteThreads, smem, s, p);
+}
+
+uw_status launch_route(const RouteParams& p, const RoutePlan& r, cudaStream_t s) {
+  uw_status st;
+  if (p.E <= 32) st = launch_route_epl<1>(p, r, s);
+  else if (p.E <= 64) st = launch_route_epl<2>(p, r, s);
+  else if (p.E <= 128) st = launch_route_epl<4>(p, r, s);
+  else if (p.E <= 256) st = launch_route_epl<8>(p, r, s);
+  else st = launch_route_epl<kMaxExperts / 32>(p, r, s);
+  if (st != UW_OK || r.blocks == 1) return st;
+  return launch_pdl(place_kernel, static_cast<unsigned>(r.blocks), kRouteThreads, static_cast<size_t>(5 * p.E + 1) * 4,
+                    s, p);
+}
+
+// ------------------------------- combine -------------------------------------
+// y[t] = r[t] + sum_j w[t, j] part[slots[t, j]], FP32 sums in order of j, one
+// rounding.  Bound by HBM: every part is read once.  A thread owns VEC
+// columns of one token and has the loads of up to four parts in flight.
+struct CombineParams {
+  const void* parts;
+  const int32_t* slots;
+  const float* weights;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* y;
+  int T, k, cols, n_rows, col_blocks;
+};
+
+template <int VEC, bool FP32>
+__device__ __forceinline__ void load_part(const void* parts, int64_t i, float (&v)[VEC]) {
+  if constexpr (FP32) {
+    const float* src = static_cast<const float*>(parts) + i;
+    if constexpr (VEC == 1) {
+      v[0] = __ldcs(src);
+    } else {
+#pragma unroll
+      for (int q = 0; q < VEC / 4; ++q) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(src) + q);
+        v[4 * q] = f.x;
+        v[4 * q + 1] = f.y;
+        v[4 * q + 2] = f.z;
+        v[4 * q + 3] = f.w;
+      }
+    }
+  } else {
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(parts) + i;
+    if constexpr (VEC == 1) {
+      v[0] = __bfloat162float(src[0]);
+    } else {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __uint_as_float(w[q] << 16);
+        v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+template <int VEC, bool FP32>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x / p.col_blocks;
+  const int c = ((blockIdx.x - t * p.col_blocks) * 256 + threadIdx.x) * VEC;
+  if (c >= p.cols) return;
+  float sum[VEC];
+  const int64_t at = static_cast<int64_t>(t) * p.cols + c;
+  if (p.residual) load_part<VEC, false>(p.residual, at, sum);
+  else
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+  const int32_t* slots = p.slots + static_cast<int64_t>(t) * p.k;
+  const float* weights = p.weights + static_cast<int64_t>(t) * p.k;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < p.k; j0 += 4) {
+    float v[4][VEC], w[4];
+    bool have[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int s = j0 + q < p.k ? __ldg(slots + j0 + q) : -1;
+      have[q] = s >= 0 && s < p.n_rows;
+      if (have[q]) {
+        w[q] = __ldg(weights + j0 + q);
+        load_part<VEC, FP32>(p.parts, static_cast<int64_t>(s) * p.cols + c, v[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (have[q])
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[q], v[q][i], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sum[i] += acc[i];
+  if constexpr (VEC == 1) {
+    p.y[at] = __float2bfloat16_rn(sum[0]);
+  } else {
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(sum[2 * q], sum[2 * q + 1]);
+      o[q] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p.y + at) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+uw_status launch_combine(const void* parts, int fp32, const int32_t* slots, const float* weights, int32_t T, int32_t k,
+                         int64_t cols, int32_t n_rows, const uint16_t* residual, uint16_t* y, cudaStream_t s) {
+  if (T < 0 || T > UW_MAX_TOKENS || k < 1 || k > UW_MAX_TOP_K || n_rows < 0 || cols < 1) return UW_ERR_INVALID_ARG;
+  if (fp32 != UW_OUT_BF16 && fp32 != UW_OUT_FP32) return UW_ERR_INVALID_ARG;
+  if (T == 0) return UW_OK;
+  if ((!parts && n_rows > 0) || !slots || !weights || !y || !aligned_to(parts, fp32 ? 4 : 2) || !aligned_to(slots, 4) ||
+      !aligned_to(weights, 4) || !aligned_to(residual, 2) || !aligned_to(y, 2))
+    return UW_ERR_INVALID_ARG;
+  // 16-byte accesses where every row starts on 16 bytes, else one value each
+  const int vec = cols % 8 == 0 && aligned16(parts) && aligned16(residual) && aligned16(y) ? 8 : 1;
+  const int64_t col_blocks = (cols + 256 * vec - 1) / (256 * vec);
+  if (cols > (int64_t(1) << 30) || col_blocks * T > 0x7FFFFFFF) return UW_ERR_UNSUPPORTED_SHAPE;
+  DeviceInfo dev;
+  const uw_status st = device_info(&dev);
+  if (st != UW_OK) return st;
+  CombineParams p;
+  p.parts = parts;
+  p.slots = slots;
+  p.weights = weights;
+  p.residual = reinterpret_cast<const __nv_bfloat16*>(residual);
+  p.y = reinterpret_cast<__nv_bfloat16*>(y);
+  p.T = T;
+  p.k = k;
+  p.cols = static_cast<int>(cols);
+  p.n_rows = n_rows;
+  p.col_blocks = static_cast<int>(col_blocks);
+  const unsigned grid = static_cast<unsigned>(col_blocks * T);
+  if (vec == 8)
+    return fp32 ? launch_pdl(combine_kernel<8, true>, grid, 256, 0, s, p)
+                : launch_pdl(combine_kernel<8, false>, grid, 256, 0, s, p);
+  return fp32 ? launch_pdl(combine_kernel<1, true>, grid, 256, 0, s, p)
+              : launch_pdl(combine_kernel<1, false>, grid, 256, 0, s, p);
+}
+
+uw_status route(const void* logits, int32_t logits_type, int32_t T, int32_t E, int32_t k, int32_t renormalize,
+                float* weights, int32_t* experts, int32_t* slots, int32_t* rows, int32_t* offsets, void* ws,
+                size_t ws_bytes, cudaStream_t s) {
+  RoutePlan r;
+  if (!route_plan(T, E, k, &r) || (logits_type != UW_OUT_BF16 && logits_type != UW_OUT_FP32)) return UW_ERR_INVALID_ARG;
+  if (!offsets || !ws || !aligned_to(offsets, 4) || !aligned16(ws)) return UW_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !weights || !experts || !slots || !rows ||
+                !aligned_to(logits, logits_type == UW_OUT_FP32 ? 4 : 2) || !aligned_to(weights, 4) ||
+                !aligned_to(experts, 4) || !aligned_to(slots, 4) || !aligned_to(rows, 4)))
+    return UW_ERR_INVALID_ARG;
+  if (ws_bytes < r.bytes) return UW_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo dev;
+  const uw_status st = device_info(&dev);
+  if (st != UW_OK) return st;
+  RouteParams p;
+  p.logits = logits;
+  p.fp32 = logits_type == UW_OUT_FP32;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.renormalize = renormalize != 0;
+  p.tokens_per_block = r.tokens_per_block;
+  p.weights = weights;
+  p.experts = experts;
+  p.slots = slots;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kWsHeader + kCounterBytes);
+  return launch_route(p, r, s);
+}
+
+// Workspace of the block: the largest grouped product's (the router's counts
+// share it), then the routing, the hidden rows and the experts' outputs.
+struct MoeWs {
+  size_t base = 0, weights = 0, experts = 0, slots = 0, rows = 0, offsets = 0, h = 0, parts = 0, total = 0;
+};
+bool moe_ws(const uw_experts* gate, const uw_experts* up, const uw_experts* down, int64_t T, int64_t k, MoeWs* out) {
+  if (!gate || !up || !down) return false;
+  if (up->n_experts != gate->n_experts || down->n_experts != gate->n_experts || up->rows != gate->rows ||
+      up->cols != gate->cols || down->rows != gate->cols || down->cols != gate->rows)
+    return false;
+  RoutePlan r;
+  if (!route_plan(T, gate->n_experts, k, &r)) return false;
+  const int64_t n = T * k;
+  if (n > UW_MAX_SLOTS) return false;
+  const size_t a = grouped_ws_bytes(gate->rows, gate->cols, gate->n_experts, static_cast<int>(n), 2);
+  const size_t b = grouped_ws_bytes(down->rows, down->cols, gate->n_experts, static_cast<int>(n), 1);
+  if (!a || !b) return false;
+  MoeWs w;
+  size_t at = align_up(std::max({a, b, r.bytes}), 256);
+  w.base = at;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(std::max<size_t>(bytes, 1), 256);
+    return here;
+  };
+  w.weights = take(static_cast<size_t>(n) * 4);
+  w.experts = take(static_cast<size_t>(n) * 4);
+  w.slots = take(static_cast<size_t>(n) * 4);
+  w.rows = take(static_cast<size_t>(n) * 4);
+  w.offsets = take(static_cast<size_t>(gate->n_experts + 1) * 4);
+  w.h = take(static_cast<size_t>(n) * gate->rows * 2);
+  w.parts = take(static_cast<size_t>(n) * down->rows * 4);
+  w.total = at;
+  *out = w;
+  return true;
+}
+
+}  // namespace
+}  // namespace uw
+
+using namespace uw;
+
+extern "C" size_t uw_moe_route_workspace_bytes(int32_t n_tokens, int32_t n_experts, int32_t top_k) {
+  RoutePlan r;
+  return route_plan(n_tokens, n_experts, top_k, &r) ? r.bytes : 0;
+}
+
+extern "C" uw_status uw_moe_route(const void* logits, int32_t logits_type, int32_t n_tokens, int32_t n_experts,
+                                  int32_t top_k, int32_t renormalize, float* weights, int32_t* experts, int32_t* slots,
+                                  int32_t* rows, int32_t* offsets, void* ws, size_t ws_bytes, void* stream) {
+  return route(logits, logits_type, n_tokens, n_experts, top_k, renormalize, weights, experts, slots, rows, offsets, ws,
+               ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" uw_status uw_moe_combine(const void* parts, int32_t parts_type, const int32_t* slots, const float* weights,
+                                    int32_t n_tokens, int32_t top_k, int64_t cols, int32_t n_rows,
+                                    const uint16_t* residual, uint16_t* y, void* stream) {
+  return launch_combine(parts, parts_type, slots, weights, n_tokens, top_k, cols, n_rows, residual, y,
+                        static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t uw_moe_workspace_bytes(const uw_experts* gate, const uw_experts* up, const uw_experts* down,
+                                         int32_t n_tokens, int32_t top_k) {
+  MoeWs w;
+  return moe_ws(gate, up, down, n_tokens, top_k, &w) ? w.total : 0;
+}
+
+extern "C" uw_status uw_moe_block(const uw_experts* gate, const uw_experts* up, const uw_experts* down,
+                                  const void* logits, int32_t logits_type, int32_t top_k, int32_t renormalize,
+                                  const uint16_t* x, int32_t n_tokens, const uint16_t* residual, uint16_t* y, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  MoeWs w;
+  if (!moe_ws(gate, up, down, n_tokens, top_k, &w)) return UW_ERR_INVALID_ARG;
+  if (!gate->table || !up->table || !down->table || !ws || !aligned16(ws)) return UW_ERR_INVALID_ARG;
+  if (n_tokens == 0) return UW_OK;
+  if (!x || !y || !logits || !aligned16(x) || !aligned_to(y, 2) || !aligned_to(residual, 2)) return UW_ERR_INVALID_ARG;
+  if (ws_bytes < w.total) return UW_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float* weights = reinterpret_cast<float*>(base + w.weights);
+  int32_t* slots = reinterpret_cast<int32_t*>(base + w.slots);
+  int32_t* rows = reinterpret_cast<int32_t*>(base + w.rows);
+  int32_t* offsets = reinterpret_cast<int32_t*>(base + w.offsets);
+  const int32_t n = n_tokens * top_k;
+  uw_status st = route(logits, logits_type, n_tokens, gate->n_experts, top_k, renormalize, weights,
+                       reinterpret_cast<int32_t*>(base + w.experts), slots, rows, offsets, ws, w.base, s);
+  if (st != UW_OK) return st;
+  GroupedArgs a;
+  a.N = gate->rows;
+  a.K = gate->cols;
+  a.E = gate->n_experts;
+  a.swiglu = true;
+  a.table[0] = gate->table;
+  a.table[1] = up->table;
+  a.x = x;
+  a.x_rows = n_tokens;
+  a.rows = rows;
+  a.offsets = offsets;
+  a.n_rows = n;
+  a.y = base + w.h;
+  a.ws = ws;
+  a.ws_bytes = w.base;
+  if ((st = launch_grouped(a, s)) != UW_OK) return st;
+  GroupedArgs d;
+  d.N = down->rows;
+  d.K = down->cols;
+  d.E = gate->n_experts;
+  d.table[0] = down->table;
+  d.x = reinterpret_cast<const uint16_t*>(base + w.h);
+  d.x_rows = n;
+  d.offsets = offsets;
+  // the router finished before the gate/up product began to let this kernel
+  // in, so the groups are known and the weights stream at once
+  d.offsets_ready = true;
+  d.n_rows = n;
+  d.out_type = UW_OUT_FP32;  // each part is rounded once, after the weighted sum
+  d.y = base + w.parts;
+  d.ws = ws;
+  d.ws_bytes = w.base;
+  if ((st = launch_grouped(d, s)) != UW_OK) return st;
+  return launch_combine(base + w.parts, UW_OUT_FP32, slots, weights, n_tokens, top_k, down->rows, n, residual, y, s);
+}

@@ -57,6 +57,18 @@ class Matrix(C.Structure):
                 ("pack_off", C.c_void_p)]
 
 
+class Epilogue(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("residual", C.c_void_p), ("activation", C.c_int32), ("out_type", C.c_int32)]
+
+
+class ExpertTable(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("reserved", C.c_int32), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("table", C.c_void_p)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+OUT_BF16, OUT_FP32 = 0, 1
+
 _P = C.c_void_p
 _SIGS = {
     "uw_build_palette_codebook": (C.c_int, [_P, C.c_int64, C.c_int64, C.POINTER(Codebook)]),
@@ -94,6 +106,24 @@ _SIGS = {
                                _P, C.c_size_t, _P]),
     "uw_autotune": (C.c_int, [C.POINTER(Matrix), C.POINTER(C.c_int32), C.c_int32, C.c_int32, _P, _P, _P,
                               C.c_size_t, _P, C.c_size_t, C.POINTER(C.c_int32), C.POINTER(C.c_float), _P]),
+    "uw_experts_table_bytes": (C.c_size_t, [C.c_int32]),
+    "uw_experts_init": (C.c_int, [C.POINTER(C.POINTER(Matrix)), C.c_int32, _P, C.c_size_t, C.POINTER(ExpertTable),
+                                  _P]),
+    "uw_grouped_workspace_bytes": (C.c_size_t, [C.POINTER(ExpertTable), C.c_int32, C.c_int32]),
+    "uw_gemm_grouped": (C.c_int, [C.POINTER(ExpertTable), _P, C.c_int32, _P, _P, C.c_int32, C.POINTER(Epilogue), _P,
+                                  _P, C.c_size_t, _P]),
+    "uw_gemm_grouped_swiglu": (C.c_int, [C.POINTER(ExpertTable), C.POINTER(ExpertTable), _P, C.c_int32, _P, _P,
+                                         C.c_int32, _P, _P, C.c_size_t, _P]),
+    "uw_gemm_epilogue_workspace_bytes": (C.c_size_t, [C.POINTER(Layout), C.c_int32]),
+    "uw_gemm_epilogue": (C.c_int, [C.POINTER(Matrix), _P, C.c_int32, C.POINTER(Epilogue), _P, _P, C.c_size_t, _P]),
+    "uw_moe_route_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32]),
+    "uw_moe_route": (C.c_int, [_P, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _P, _P, _P, _P, _P, _P,
+                               C.c_size_t, _P]),
+    "uw_moe_combine": (C.c_int, [_P, C.c_int32, _P, _P, C.c_int32, C.c_int32, C.c_int64, C.c_int32, _P, _P, _P]),
+    "uw_moe_workspace_bytes": (C.c_size_t, [C.POINTER(ExpertTable), C.POINTER(ExpertTable), C.POINTER(ExpertTable),
+                                            C.c_int32, C.c_int32]),
+    "uw_moe_block": (C.c_int, [C.POINTER(ExpertTable), C.POINTER(ExpertTable), C.POINTER(ExpertTable), _P, C.c_int32,
+                               C.c_int32, C.c_int32, _P, C.c_int32, _P, _P, _P, C.c_size_t, _P]),
     "uw_status_string": (C.c_char_p, [C.c_int]),
     "uw_version": (C.c_int32, []),
     "uw_launch_count": (C.c_uint64, []),
@@ -469,6 +499,202 @@ def mlp_stack(layers, pipelines, x, y, ws: Workspace, stream=None):
     arr, pipes, n = _stack_args(layers, pipelines)
     _check(lib().uw_mlp_stack(arr, pipes, n, _ptr(x), x.shape[0], _ptr(y), ws.ptr, ws.nbytes, _stream(stream)),
            "uw_mlp_stack")
+
+
+# ---------------------------------------------------------------------------
+# products grouped by expert, fused epilogues, mixture of experts
+# ---------------------------------------------------------------------------
+# These calls check their tensors (shape, type, contiguity, device) and run on
+# the tensors' device; a mismatch raises UwError(UW_ERR_INVALID_ARG) before
+# anything is launched.  BF16 tensors may be torch.bfloat16 or, as elsewhere
+# in this module, int16 views of it.
+
+_BF16, _FP32, _INT32 = ("torch.bfloat16", "torch.int16"), ("torch.float32",), ("torch.int32",)
+
+
+def _tensor(t, what, types, shape, device):
+    """Checks a tensor argument; None stays None."""
+    if t is None:
+        return None
+    if str(t.dtype) not in types or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a contiguous {' or '.join(types)} {tuple(shape)} on {device} is "
+                                          f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _matrix_of(t, what):
+    """[rows, cols] of a 2-D tensor argument."""
+    if t is None or t.dim() != 2:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a 2-D tensor is wanted")
+    return t.shape
+
+
+def _out_type(t, what):
+    if str(t.dtype) in _BF16:
+        return OUT_BF16
+    if str(t.dtype) in _FP32:
+        return OUT_FP32
+    raise UwError(UW_ERR_INVALID_ARG, f"{what}: BF16 or FP32 is wanted, got {t.dtype}")
+
+
+def _call(fn, what, device, stream, *args):
+    """One library call on `device`, whichever is current."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _check(fn(*args, _stream(stream)), what)
+    _check(fn(*args, _stream(stream)), what)
+
+
+class Experts:
+    """One compressed matrix per expert (same shape, direct-palette form), as
+    the grouped products take them (uw_experts_init).  Keeps the matrices."""
+
+    def __init__(self, matrices, stream=None):
+        import torch
+        self.matrices = list(matrices)
+        if not self.matrices:
+            raise UwError(UW_ERR_INVALID_ARG, "Experts: no matrices")
+        self.device = self.matrices[0].sm.device
+        if any(m.sm.device != self.device for m in self.matrices):
+            raise UwError(UW_ERR_INVALID_ARG, "Experts: matrices on different devices")
+        n = len(self.matrices)
+        nbytes = int(lib().uw_experts_table_bytes(n))
+        self.table = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+        self.c = ExpertTable()
+        arr = (C.POINTER(Matrix) * n)(*[C.pointer(m.mat) for m in self.matrices])
+        _call(lib().uw_experts_init, "uw_experts_init", self.device, stream, arr, n, self.table.data_ptr(), nbytes,
+              C.byref(self.c))
+
+    def __len__(self):
+        return int(self.c.n_experts)
+
+    @property
+    def rows(self):
+        return int(self.c.rows)
+
+    @property
+    def cols(self):
+        return int(self.c.cols)
+
+
+def grouped_workspace_bytes(experts: Experts, n_rows: int, swiglu: bool = False) -> int:
+    return int(lib().uw_grouped_workspace_bytes(C.byref(experts.c), n_rows, int(swiglu)))
+
+
+def epilogue_workspace_bytes(dm_or_layout, batch: int) -> int:
+    L = dm_or_layout.mat.L if isinstance(dm_or_layout, DeviceMatrix) else dm_or_layout
+    return int(lib().uw_gemm_epilogue_workspace_bytes(C.byref(L), batch))
+
+
+def _epilogue(device, n_groups, n_rows, rows, y, bias, activation, residual):
+    if activation not in ACTIVATIONS:
+        raise UwError(UW_ERR_INVALID_ARG, f"activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
+    out = _out_type(y, "y")
+    e = Epilogue(_tensor(bias, "bias", _BF16, (rows,) if n_groups is None else (n_groups, rows), device),
+                 _tensor(residual, "residual", _BF16, (n_rows, rows), device), ACTIVATIONS[activation], out)
+    return e, _tensor(y, "y", _BF16 if out == OUT_BF16 else _FP32, (n_rows, rows), device)
+
+
+def gemm_epilogue(dm: DeviceMatrix, x, y, ws: Workspace, bias=None, activation: str = "none", residual=None,
+                  stream=None):
+    """y = act(x W^T + bias) + residual (uw_gemm_epilogue): x BF16 [batch,
+    cols], y BF16 or FP32 [batch, rows], bias BF16 [rows], residual BF16
+    [batch, rows]."""
+    batch, _ = _matrix_of(x, "x")
+    dev = dm.sm.device
+    e, yp = _epilogue(dev, None, batch, dm.rows, y, bias, activation, residual)
+    _call(lib().uw_gemm_epilogue, "uw_gemm_epilogue", dev, stream, C.byref(dm.mat),
+          _tensor(x, "x", _BF16, (batch, dm.cols), dev), batch, C.byref(e), yp, ws.ptr, ws.nbytes)
+
+
+def _groups(experts, x, offsets, n_rows, rows):
+    dev = experts.device
+    x_rows, _ = _matrix_of(x, "x")
+    return (_tensor(x, "x", _BF16, (x_rows, experts.cols), dev), x_rows, _tensor(rows, "rows", _INT32, (n_rows,), dev),
+            _tensor(offsets, "offsets", _INT32, (len(experts) + 1,), dev), n_rows)
+
+
+def gemm_grouped(experts: Experts, x, offsets, y, ws: Workspace, rows=None, bias=None, activation: str = "none",
+                 residual=None, stream=None):
+    """y[s] = act(x[rows[s]] W_e^T + bias[e]) + residual[s] for the slots s in
+    [offsets[e], offsets[e+1]) of each expert e (uw_gemm_grouped): y BF16 or
+    FP32 [n_rows, rows of W], bias BF16 [n_experts, rows of W]."""
+    n_rows, _ = _matrix_of(y, "y")
+    e, yp = _epilogue(experts.device, len(experts), n_rows, experts.rows, y, bias, activation, residual)
+    _call(lib().uw_gemm_grouped, "uw_gemm_grouped", experts.device, stream, C.byref(experts.c),
+          *_groups(experts, x, offsets, n_rows, rows), C.byref(e), yp, ws.ptr, ws.nbytes)
+
+
+def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace, rows=None, stream=None):
+    """h[s] = SiLU(x[rows[s]] G_e^T) * (x[rows[s]] U_e^T) (uw_gemm_grouped_swiglu):
+    h BF16 [n_rows, rows of G]."""
+    n_rows, _ = _matrix_of(h, "h")
+    if up.device != gate.device:
+        raise UwError(UW_ERR_INVALID_ARG, "gate and up on different devices")
+    _call(lib().uw_gemm_grouped_swiglu, "uw_gemm_grouped_swiglu", gate.device, stream, C.byref(gate.c), C.byref(up.c),
+          *_groups(gate, x, offsets, n_rows, rows), _tensor(h, "h", _BF16, (n_rows, gate.rows), gate.device), ws.ptr,
+          ws.nbytes)
+
+
+class Route:
+    """Where uw_moe_route leaves its results (torch tensors own memory)."""
+
+    def __init__(self, n_tokens: int, n_experts: int, top_k: int, device="cuda"):
+        import torch
+        self.n_tokens, self.n_experts, self.top_k = n_tokens, n_experts, top_k
+        self.weights = torch.empty(n_tokens, top_k, dtype=torch.float32, device=device)
+        self.experts = torch.empty(n_tokens, top_k, dtype=torch.int32, device=device)
+        self.slots = torch.empty(n_tokens, top_k, dtype=torch.int32, device=device)
+        self.rows = torch.empty(n_tokens * top_k, dtype=torch.int32, device=device)
+        self.offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=device)
+        self.device = self.weights.device
+
+
+def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:
+    return int(lib().uw_moe_route_workspace_bytes(n_tokens, n_experts, top_k))
+
+
+def moe_route(logits, route: Route, ws: Workspace, renormalize: bool = True, stream=None):
+    """Top-k routing of logits [n_tokens, n_experts] (BF16 or FP32) into
+    `route` (uw_moe_route)."""
+    typ = _out_type(logits, "logits")
+    lp = _tensor(logits, "logits", _BF16 if typ == OUT_BF16 else _FP32, (route.n_tokens, route.n_experts), route.device)
+    _call(lib().uw_moe_route, "uw_moe_route", route.device, stream, lp, typ, route.n_tokens, route.n_experts,
+          route.top_k, int(renormalize), route.weights.data_ptr(), route.experts.data_ptr(), route.slots.data_ptr(),
+          route.rows.data_ptr(), route.offsets.data_ptr(), ws.ptr, ws.nbytes)
+
+
+def moe_combine(parts, slots, weights, y, residual=None, stream=None):
+    """y[t] = residual[t] + sum_j weights[t, j] parts[slots[t, j]]
+    (uw_moe_combine): parts FP32 or BF16 [n_rows, cols]."""
+    n_rows, cols = _matrix_of(parts, "parts")
+    n_tokens, top_k = _matrix_of(slots, "slots")
+    dev, typ = parts.device, _out_type(parts, "parts")
+    _call(lib().uw_moe_combine, "uw_moe_combine", dev, stream,
+          _tensor(parts, "parts", _BF16 if typ == OUT_BF16 else _FP32, (n_rows, cols), dev), typ,
+          _tensor(slots, "slots", _INT32, (n_tokens, top_k), dev),
+          _tensor(weights, "weights", _FP32, (n_tokens, top_k), dev), n_tokens, top_k, cols, n_rows,
+          _tensor(residual, "residual", _BF16, (n_tokens, cols), dev), _tensor(y, "y", _BF16, (n_tokens, cols), dev))
+
+
+def moe_workspace_bytes(gate: Experts, up: Experts, down: Experts, n_tokens: int, top_k: int) -> int:
+    return int(lib().uw_moe_workspace_bytes(C.byref(gate.c), C.byref(up.c), C.byref(down.c), n_tokens, top_k))
+
+
+def moe_block(gate: Experts, up: Experts, down: Experts, x, logits, top_k: int, y, ws: Workspace, residual=None,
+              renormalize: bool = True, stream=None):
+    """Sparse SwiGLU MLP block (uw_moe_block): y[t] = residual[t] + sum over
+    token t's top_k experts of weight * W_down (SiLU(W_gate x) * (W_up x))."""
+    n_tokens, _ = _matrix_of(x, "x")
+    dev, typ = gate.device, _out_type(logits, "logits")
+    if up.device != dev or down.device != dev:
+        raise UwError(UW_ERR_INVALID_ARG, "gate, up and down on different devices")
+    shape = (n_tokens, gate.cols)
+    _call(lib().uw_moe_block, "uw_moe_block", dev, stream, C.byref(gate.c), C.byref(up.c), C.byref(down.c),
+          _tensor(logits, "logits", _BF16 if typ == OUT_BF16 else _FP32, (n_tokens, len(gate)), dev), typ, top_k,
+          int(renormalize), _tensor(x, "x", _BF16, shape, dev), n_tokens,
+          _tensor(residual, "residual", _BF16, shape, dev), _tensor(y, "y", _BF16, shape, dev), ws.ptr, ws.nbytes)
 
 
 def autotune(dm: DeviceMatrix, batches, reps: int, x, y, ws: Workspace, flush=None, stream=None):

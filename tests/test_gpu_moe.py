@@ -1,0 +1,348 @@
+"""GPU: router, weighted combination and the sparse MLP block against float64
+forms written from their definitions."""
+import math
+
+import numpy as np
+import pytest
+
+from mlp_huffman_coded_b200 import synth
+from mlp_huffman_coded_b200 import uw
+from oracle import uw_oracle as O
+
+from gpu_util import bf16_f64, device_matrix, empty_bf16, to_dev, to_host_u16
+from moe_util import F32, HALF_ULP, expert_weights, product, route_ref, sum_bound
+
+pytestmark = pytest.mark.gpu
+
+
+def run_route(logits, k, renormalize=True, bf16=False):
+    import torch
+    T, E = logits.shape
+    l = torch.from_numpy(np.ascontiguousarray(logits, dtype=np.float32)).cuda()
+    r = uw.Route(T, E, k)
+    r.rows.fill_(-7)
+    ws = uw.Workspace(uw.route_workspace_bytes(T, E, k))
+    uw.moe_route(l.to(torch.bfloat16) if bf16 else l, r, ws, renormalize=renormalize)
+    ws.check("route")
+    return r
+
+
+def check_route(r, logits, k, renormalize=True):
+    w, e, s, rows, off = route_ref(logits, k, renormalize)
+    assert np.array_equal(r.experts.cpu().numpy(), e)
+    assert np.array_equal(r.offsets.cpu().numpy(), off)
+    assert np.array_equal(r.slots.cpu().numpy(), s)
+    n = int(off[-1])
+    got = r.rows.cpu().numpy()
+    assert np.array_equal(got[:n], rows)
+    assert np.all(got[n:] == -7)  # entries past the last slot stay as they were
+    # expf is off by at most 2 units in the last place plus its argument's
+    # rounding (2^-24 |l - max|, and a weight with |l - max| > 88 is below
+    # any that matters: 1e-38); the sum adds E roundings, the quotient one
+    bound = (len(logits[0]) + 8 + 2 * 88) * F32 * w + 1e-37
+    assert np.all(np.abs(r.weights.cpu().numpy().astype(np.float64) - w) <= bound)
+
+
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 129, 700])
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (8, 2), (33, 5), (64, 8), (130, 3), (256, 8), (1000, 32)])
+def test_route_against_float64(T, E, k):
+    logits = np.random.default_rng(T * 1000 + E).standard_normal((T, E)).astype(np.float32) * 2
+    for ren in (True, False):
+        check_route(run_route(logits, k, ren), logits, k, ren)
+
+
+def test_route_bf16_logits_tie_often():
+    logits = synth.bf16_bits_to_f32(synth.f32_to_bf16_bits(
+        np.round(np.random.default_rng(3).standard_normal((300, 40)) * 4).astype(np.float32)))
+    logits[5] = 0.0
+    logits[6, ::2] = -0.0
+    check_route(run_route(logits, 6, bf16=True), logits, 6)
+
+
+def test_route_masked_rows_infinities_and_nans():
+    rng = np.random.default_rng(4)
+    logits = rng.standard_normal((200, 16)).astype(np.float32)
+    low = np.finfo(np.float32).min
+    logits[3] = -np.inf                       # nothing left
+    logits[4, 1:] = -np.inf                   # one expert left
+    logits[5] = np.nan
+    logits[6, ::3] = np.nan
+    logits[7, 2] = logits[7, 9] = np.inf      # share the weight
+    logits[8] = low                           # the type's lowest value is a value
+    logits[9, :8] = low
+    logits[150:] = -np.inf                    # a padded batch
+    for ren in (True, False):
+        check_route(run_route(logits, 4, ren), logits, 4, ren)
+
+
+def test_route_every_token_to_one_expert_and_none_at_all():
+    logits = np.full((500, 12), -np.inf, np.float32)
+    check_route(run_route(logits, 2), logits, 2)
+    logits[:, 7] = 1.0
+    check_route(run_route(logits, 2), logits, 2)
+
+
+def test_route_no_tokens():
+    r = uw.Route(0, 8, 2)
+    r.offsets.fill_(5)
+    ws = uw.Workspace(uw.route_workspace_bytes(0, 8, 2))
+    import torch
+    uw.moe_route(torch.empty(0, 8, device="cuda"), r, ws)
+    ws.check()
+    assert r.offsets.tolist() == [0] * 9
+
+
+def test_route_more_tokens_than_one_chunk_per_block():
+    """20000 tokens: every block ranks several runs of 64."""
+    logits = np.random.default_rng(5).standard_normal((20000, 8)).astype(np.float32)
+    check_route(run_route(logits, 2), logits, 2)
+
+
+# ------------------------------- combine -------------------------------------
+
+def combine_check(parts, slots, weights, residual, y, bf16_parts):
+    p = O.bf16_to_f64(parts) if bf16_parts else parts.astype(np.float64)
+    n = p.shape[0]
+    T, k = slots.shape
+    ref = np.zeros((T, p.shape[1])) if residual is None else O.bf16_to_f64(residual).copy()
+    size = np.abs(ref)
+    for j in range(k):
+        for t in range(T):
+            if 0 <= slots[t, j] < n:
+                v = float(weights[t, j]) * p[slots[t, j]]
+                ref[t] += v
+                size[t] += np.abs(v)
+    d = (k + 1) * F32 * size  # k fused multiply-adds and one addition
+    d = d + HALF_ULP * (np.abs(ref) + d) + 1e-38
+    assert np.all(np.abs(y - ref) <= d)
+
+
+@pytest.mark.parametrize("cols", [1, 7, 8, 264, 2048, 4100])
+@pytest.mark.parametrize("T,k", [(1, 1), (3, 2), (65, 5), (40, 9)])
+@pytest.mark.parametrize("bf16_parts", [False, True])
+def test_combine_against_float64(cols, T, k, bf16_parts):
+    import torch
+    rng = np.random.default_rng(cols + T)
+    n = T * k
+    parts = rng.standard_normal((n, cols)).astype(np.float32)
+    if bf16_parts:
+        parts = synth.f32_to_bf16_bits(parts)
+    slots = rng.permutation(n).reshape(T, k).astype(np.int32)
+    slots[0, 0] = -1
+    if T > 2:
+        slots[2] = -1        # no expert at all: the residual, or zero
+        slots[1, 1] = n      # outside: adds nothing
+        slots[1, 0] = slots[0, 1]
+    weights = rng.random((T, k)).astype(np.float32)
+    weights[0, 0] = np.nan   # of a slot that is not there
+    res = synth.activations(T, cols, 7)
+    for r in (None, res):
+        y = empty_bf16(T, cols)
+        uw.moe_combine(to_dev(parts), to_dev(slots), torch.from_numpy(weights).cuda(), y,
+                       residual=None if r is None else to_dev(r))
+        combine_check(parts, slots, weights, r, bf16_f64(to_host_u16(y)), bf16_parts)
+    r = to_dev(res)
+    uw.moe_combine(to_dev(parts), to_dev(slots), torch.from_numpy(weights).cuda(), r, residual=r)
+    assert np.array_equal(to_host_u16(r), to_host_u16(y))  # in place
+
+
+def test_combine_of_unaligned_slices():
+    import torch
+    T, k, cols = 6, 2, 256
+    rng = np.random.default_rng(8)
+    parts = rng.standard_normal((T * k, cols)).astype(np.float32)
+    res = synth.activations(T, cols, 9)
+    slots = rng.permutation(T * k).reshape(T, k).astype(np.int32)
+    weights = rng.random((T, k)).astype(np.float32)
+
+    def shifted(t):  # the same values one element into a larger tensor
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        flat[1:] = t.flatten()
+        return flat[1:].view(t.shape)
+
+    y = shifted(empty_bf16(T, cols))
+    uw.moe_combine(shifted(to_dev(parts)), shifted(to_dev(slots)), shifted(torch.from_numpy(weights).cuda()), y,
+                   residual=shifted(to_dev(res)))
+    combine_check(parts, slots, weights, res, bf16_f64(to_host_u16(y)), False)
+
+
+# -------------------------------- block --------------------------------------
+
+def block_ref(gs, us, ds, x, logits, k, residual, renormalize=True):
+    """(y, bound): h rounded to BF16 once (HALF_ULP), sums as bounded for the
+    single products, weights within the router's bound."""
+    w, e, _, _, _ = route_ref(logits, k, renormalize)
+    T, d = x.shape
+    ref = np.zeros((T, d)) if residual is None else O.bf16_to_f64(residual).copy()
+    bound = F32 * np.abs(ref)
+    for t in range(T):
+        for j in range(k):
+            if e[t, j] < 0:
+                continue
+            xt = x[t:t + 1]
+            g, ag = product(gs[e[t, j]], xt)
+            u, au = product(us[e[t, j]], xt)
+            K = x.shape[1]
+            dg, du = sum_bound(ag, K), sum_bound(au, K)
+            s = O.silu(g)
+            h = s * u
+            dh = 1.1 * dg * np.abs(u) + np.abs(s) * du + 1.1 * dg * du + 16 * F32 * (np.abs(g) + np.abs(s)) * np.abs(u)
+            dh = dh + HALF_ULP * (np.abs(h) + dh)
+            wd = O.bf16_to_f64(ds[e[t, j]])
+            part = (h @ wd.T)[0]
+            ab = ((np.abs(h) + dh) @ np.abs(wd).T)[0]
+            dpart = (dh @ np.abs(wd).T)[0] + sum_bound(ab, wd.shape[1])
+            dw = (logits.shape[1] + 8 + 176) * F32 * w[t, j]
+            ref[t] += w[t, j] * part
+            bound[t] += w[t, j] * dpart + dw * (np.abs(part) + dpart) + 4 * F32 * w[t, j] * (np.abs(part) + dpart)
+    bound = bound + (k + 1) * F32 * np.abs(ref)
+    return ref, bound + HALF_ULP * (np.abs(ref) + bound) + 1e-30
+
+
+def experts_of(mats):
+    return uw.Experts([device_matrix(m) for m in mats])
+
+
+@pytest.fixture(scope="module")
+def sparse_mlp():
+    E, d, ffn = 6, 256, 320
+    mats = expert_weights(E, ffn, d, 600), expert_weights(E, ffn, d, 620), expert_weights(E, d, ffn, 640)
+    return mats, [experts_of(m) for m in mats]
+
+
+@pytest.mark.parametrize("T", [1, 2, 17, 150])
+@pytest.mark.parametrize("k", [1, 2, 6])
+def test_block_against_float64(sparse_mlp, T, k):
+    import torch
+    (gs, us, ds), ex = sparse_mlp
+    d = ds[0].shape[0]
+    x = synth.activations(T, d, 660 + T)
+    logits = np.random.default_rng(T).standard_normal((T, len(gs))).astype(np.float32)
+    if T > 4:
+        logits[3] = -np.inf   # padded token: the residual passes through
+        logits[4, 1:] = -np.inf
+    res = synth.activations(T, d, 661)
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    for r, ren in ((None, True), (res, False)):
+        y = empty_bf16(T, d)
+        uw.moe_block(*ex, to_dev(x), torch.from_numpy(logits).cuda(), k, y, ws,
+                     residual=None if r is None else to_dev(r), renormalize=ren)
+        ws.check("block")
+        ref, bound = block_ref(gs, us, ds, x, logits, k, r, ren)
+        got = bf16_f64(to_host_u16(y))
+        assert np.all(np.abs(got - ref) <= bound), float(np.max(np.abs(got - ref) - bound))
+
+
+def test_block_equals_its_four_calls(sparse_mlp):
+    import torch
+    _, ex = sparse_mlp
+    T, k, d, ffn = 45, 2, ex[2].rows, ex[0].rows
+    x = to_dev(synth.activations(T, d, 670))
+    res = to_dev(synth.activations(T, d, 671))
+    logits = torch.randn(T, len(ex[0]), device="cuda")
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    y = empty_bf16(T, d)
+    uw.moe_block(*ex, x, logits, k, y, ws, residual=res)
+    r = uw.Route(T, len(ex[0]), k)
+    h, parts, y2 = empty_bf16(T * k, ffn), torch.empty(T * k, d, device="cuda"), empty_bf16(T, d)
+    uw.moe_route(logits, r, ws)
+    uw.gemm_grouped_swiglu(ex[0], ex[1], x, r.offsets, h, ws, rows=r.rows)
+    uw.gemm_grouped(ex[2], h, r.offsets, parts, ws)
+    uw.moe_combine(parts, r.slots, r.weights, y2, residual=res)
+    ws.check()
+    assert torch.equal(y, y2)
+
+
+def test_layers_chained_on_one_stream_match_layers_one_by_one(sparse_mlp):
+    """Launches overlap (a kernel starts while the one before it finishes);
+    ten blocks in a row, in place on the residual stream, equal the same
+    blocks with the device idle between them, and a dense product that
+    follows sees the last one's output."""
+    import torch
+    _, ex = sparse_mlp
+    T, k, d = 9, 2, ex[2].rows
+    x0 = to_dev(synth.activations(T, d, 680))
+    logits = torch.randn(10, T, len(ex[0]), device="cuda")
+    dm = device_matrix(synth.weight_matrix(384, d, 0.02, 1e-3, 200.0, 681))
+    ws = uw.Workspace(max(uw.moe_workspace_bytes(*ex, T, k), uw.workspace_bytes(dm, uw.PIPE_DIRECT, T)))
+
+    def chain(sync):
+        x, y = x0.clone(), empty_bf16(T, 384)
+        for l in logits:
+            uw.moe_block(*ex, x, l, k, x, ws, residual=x)
+            if sync:
+                torch.cuda.synchronize()
+        uw.gemm_direct_palette(dm, x, y, ws)
+        ws.check()
+        return x, y
+
+    slow = chain(True)
+    for _ in range(5):
+        fast = chain(False)
+        assert torch.equal(fast[0], slow[0]) and torch.equal(fast[1], slow[1])
+
+
+def test_captured_block_replays_on_new_inputs(sparse_mlp):
+    """Routing is on the device, so one captured graph serves every batch of
+    its size, whatever its groups; on another stream than the default."""
+    import torch
+    _, ex = sparse_mlp
+    T, k, d, E = 12, 2, ex[2].rows, len(ex[0])
+    side = torch.cuda.Stream()
+    x, l, y = empty_bf16(T, d), torch.empty(T, E, device="cuda"), empty_bf16(T, d)
+    with torch.cuda.stream(side):
+        ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+        x.zero_()
+        l.zero_()
+        uw.moe_block(*ex, x, l, k, y, ws)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            uw.moe_block(*ex, x, l, k, y, ws)
+    for seed in range(4):
+        x.copy_(to_dev(synth.activations(T, d, 690 + seed)))
+        l.copy_(torch.from_numpy(np.random.default_rng(seed).standard_normal((T, E)).astype(np.float32) * (1 + 4 * seed)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = empty_bf16(T, d)
+        uw.moe_block(*ex, x, l, k, want, ws)
+        ws.check()
+        assert torch.equal(y, want)
+
+
+# ------------------------- refusals on the device ----------------------------
+
+@pytest.mark.parametrize("offsets", [[0, 5, 3, 8], [-1, 2, 3, 8], [0, 2, 3, 9], [9, 9, 9, 9]])
+def test_bad_offsets_are_reported_and_nothing_is_computed(offsets):
+    import torch
+    ex = experts_of(expert_weights(3, 128, 128, 700))
+    x = to_dev(synth.activations(8, 128, 701))
+    y = torch.full((8, 128), 3.0, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, 8))
+    uw.gemm_grouped(ex, x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), y, ws)
+    assert ws.status() == uw.UW_ERR_INVALID_ARG
+    assert bool((y == 3.0).all())
+    good = torch.tensor([0, 2, 3, 8], dtype=torch.int32, device="cuda")
+    uw.gemm_grouped(ex, x, good, y, ws)
+    ws.check("after")
+
+
+def test_a_row_number_outside_x_is_reported():
+    import torch
+    mats = expert_weights(2, 128, 128, 710)
+    ex = experts_of(mats)
+    x = to_dev(synth.activations(4, 128, 711))
+    y = torch.zeros(6, 128, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, 6))
+    off = torch.tensor([0, 3, 6], dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 1, 2, 3, 0, 1], dtype=torch.int32, device="cuda")
+    uw.gemm_grouped(ex, x, off, y, ws, rows=good)
+    ws.check()
+    for bad in (4, -1, 2**31 - 1, -2**31):
+        r, z = good.clone(), torch.zeros_like(y)
+        r[4] = bad
+        uw.gemm_grouped(ex, x, off, z, ws, rows=r)
+        assert ws.status() == uw.UW_ERR_INVALID_ARG
+        keep = torch.arange(6, device="cuda") != 4
+        assert torch.equal(z[keep], y[keep])  # the other slots are right

@@ -1,0 +1,179 @@
+"""CPU: refusals and sizes of the grouped products, the fused epilogues and
+the router (nothing here reaches a device)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from mlp_huffman_coded_b200 import synth
+from mlp_huffman_coded_b200 import uw
+
+from moe_util import act_f64, route_ref
+
+P = 0x10000  # a non-NULL, aligned address that no call may reach
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    from mlp_huffman_coded_b200 import build
+    build.build()
+    return uw.lib()
+
+
+def table(n=4, rows=256, cols=512, ptr=P):
+    t = uw.ExpertTable()
+    t.n_experts, t.rows, t.cols, t.table = n, rows, cols, ptr
+    return t
+
+
+def matrix(rows=256, cols=512, pack=P):
+    enc = uw.encode(synth.weight_matrix(rows, cols, 0.02, 1e-3, 100.0, 1))
+    m = enc.matrix()
+    m._keep = enc
+    for f in ("sm", "stream", "chunk_bit_off", "vflags", "vprefix", "verbatim"):
+        setattr(m, f, P)
+    m.pack, m.pack_off = pack, pack
+    return m
+
+
+def test_structs_match_the_header():
+    assert C.sizeof(uw.Epilogue) == 24
+    assert C.sizeof(uw.ExpertTable) == 32
+    assert uw.lib().uw_experts_table_bytes(3) == 3 * 80
+    assert uw.lib().uw_experts_table_bytes(0) == 0
+    assert uw.lib().uw_experts_table_bytes(1025) == 0
+
+
+def test_workspace_sizes():
+    f = uw.lib().uw_grouped_workspace_bytes
+    t = table()
+    one = f(C.byref(t), 8, 0)
+    assert 0 < one < f(C.byref(t), 8, 1) and f(C.byref(t), 4096, 0) > one
+    assert f(None, 8, 0) == 0 and f(C.byref(t), -1, 0) == 0
+    assert f(C.byref(table(n=0)), 8, 0) == 0 and f(C.byref(table(n=2000)), 8, 0) == 0
+    assert f(C.byref(table(cols=500)), 8, 0) == 0 and f(C.byref(table(cols=1 << 16)), 8, 0) == 0
+    # more units than an index holds
+    assert f(C.byref(table(rows=1 << 20, cols=32768)), 1 << 22, 0) == 0
+    g = uw.lib().uw_gemm_epilogue_workspace_bytes
+    L = matrix().L
+    assert g(C.byref(L), 1) > 0 and g(C.byref(L), 100000) > 0 and g(C.byref(L), -1) == 0 and g(None, 1) == 0
+
+
+def test_route_sizes():
+    f = uw.lib().uw_moe_route_workspace_bytes
+    assert f(1, 8, 2) > 0 and f(0, 8, 2) > 0 and f(1 << 20, 1024, 32) > 0
+    for bad in ((-1, 8, 2), (1, 0, 1), (1, 8, 9), (1, 8, 0), (1, 64, 33), ((1 << 20) + 1, 8, 2), (1, 1025, 1)):
+        assert f(*bad) == 0
+
+
+@pytest.mark.parametrize("change", ["w", "offsets", "n_rows", "x_rows", "short_x", "table"])
+def test_grouped_refusals(change):
+    a = dict(w=C.byref(table()), x=P, x_rows=8, rows=None, offsets=P, n_rows=8)
+    if change in ("w", "offsets"):
+        a[change] = None
+    elif change == "table":
+        a["w"] = C.byref(table(ptr=P + 4))
+    elif change == "short_x":
+        a["x_rows"] = 7
+    else:
+        a[change] = -1
+    st = uw.lib().uw_gemm_grouped(a["w"], a["x"], a["x_rows"], a["rows"], a["offsets"], a["n_rows"], None, P, P, 1 << 30,
+                                  None)
+    assert st == uw.UW_ERR_INVALID_ARG
+    w = a["w"]
+    st = uw.lib().uw_gemm_grouped_swiglu(w, w, a["x"], a["x_rows"], a["rows"], a["offsets"], a["n_rows"], P, P, 1 << 30,
+                                         None)
+    assert st == uw.UW_ERR_INVALID_ARG
+
+
+def test_nothing_to_do_launches_nothing():
+    n = uw.launch_count()
+    t, m = table(), matrix()
+    lib = uw.lib()
+    assert lib.uw_gemm_grouped(C.byref(t), None, 0, None, P, 0, None, None, None, 0, None) == uw.UW_OK
+    assert lib.uw_gemm_grouped_swiglu(C.byref(t), C.byref(t), None, 0, None, P, 0, None, None, 0, None) == uw.UW_OK
+    assert lib.uw_gemm_epilogue(C.byref(m), None, 0, None, None, None, 0, None) == uw.UW_OK
+    assert lib.uw_moe_combine(None, 1, None, None, 0, 2, 64, 0, None, None, None) == uw.UW_OK
+    assert uw.launch_count() == n
+
+
+def test_swiglu_gate_and_up_must_agree():
+    for other in (table(n=3), table(rows=128), table(cols=256)):
+        st = uw.lib().uw_gemm_grouped_swiglu(C.byref(table()), C.byref(other), P, 8, None, P, 8, P, P, 1 << 30, None)
+        assert st == uw.UW_ERR_INVALID_ARG
+
+
+def test_epilogue_refusals():
+    lib = uw.lib()
+    assert lib.uw_gemm_epilogue(None, P, 1, None, P, P, 1 << 30, None) == uw.UW_ERR_INVALID_ARG
+    assert lib.uw_gemm_epilogue(C.byref(matrix()), P, -1, None, P, P, 1 << 30, None) == uw.UW_ERR_INVALID_ARG
+    assert lib.uw_gemm_epilogue(C.byref(matrix(pack=None)), P, 1, None, P, P, 1 << 30, None) == uw.UW_ERR_INVALID_ARG
+
+
+def test_experts_refusals():
+    lib = uw.lib()
+    a, b, out = matrix(), matrix(rows=128), uw.ExpertTable()
+
+    def init(mats, n=None, ptr=P, nbytes=1 << 20):
+        arr = (C.POINTER(uw.Matrix) * max(len(mats), 1))(*[C.pointer(m) if m else None for m in mats])
+        return lib.uw_experts_init(arr, len(mats) if n is None else n, ptr, nbytes, C.byref(out), None)
+
+    assert init([a, b]) == uw.UW_ERR_UNSUPPORTED_SHAPE
+    assert init([a, matrix(pack=None)]) == uw.UW_ERR_INVALID_ARG
+    assert init([a, None]) == uw.UW_ERR_INVALID_ARG
+    assert init([a], n=0) == uw.UW_ERR_INVALID_ARG and init([a], n=1025) == uw.UW_ERR_INVALID_ARG
+    assert init([a], ptr=None) == uw.UW_ERR_INVALID_ARG and init([a], ptr=P + 8) == uw.UW_ERR_INVALID_ARG
+    assert init([a, a], nbytes=159) == uw.UW_ERR_WORKSPACE_TOO_SMALL
+    a.cb.code_len[0] = 16
+    assert init([a]) == uw.UW_ERR_CORRUPT
+    with pytest.raises(uw.UwError):
+        uw.Experts([])
+
+
+def test_route_and_combine_refusals():
+    lib = uw.lib()
+
+    def route(logits=P, typ=1, T=4, E=8, k=2, w=P, off=P, ws=P, n=1 << 30):
+        return lib.uw_moe_route(logits, typ, T, E, k, 1, w, P, P, P, off, ws, n, None)
+
+    for bad in (dict(logits=None), dict(logits=P + 2), dict(typ=2), dict(T=-1), dict(E=0), dict(k=0), dict(k=9),
+                dict(w=None), dict(off=None), dict(off=P + 2), dict(ws=None)):
+        assert route(**bad) == uw.UW_ERR_INVALID_ARG, bad
+    assert route(T=1000, n=256) == uw.UW_ERR_WORKSPACE_TOO_SMALL
+
+    def combine(parts=P, typ=1, slots=P, w=P, T=4, k=2, cols=64, n=8, y=P):
+        return lib.uw_moe_combine(parts, typ, slots, w, T, k, cols, n, None, y, None)
+
+    for bad in (dict(parts=None), dict(parts=P + 2), dict(typ=5), dict(slots=None), dict(w=P + 2), dict(T=-1), dict(k=0),
+                dict(k=33), dict(cols=0), dict(n=-1), dict(y=None)):
+        assert combine(**bad) == uw.UW_ERR_INVALID_ARG, bad
+    assert combine(cols=1 << 31) == uw.UW_ERR_UNSUPPORTED_SHAPE
+
+
+def test_block_refusals():
+    lib = uw.lib()
+    g, u, d = table(rows=320, cols=256), table(rows=320, cols=256), table(rows=256, cols=320)
+    need = lib.uw_moe_workspace_bytes(C.byref(g), C.byref(u), C.byref(d), 5, 2)
+    assert need > 0
+    for bad in ((g, u, g), (g, table(n=3, rows=320, cols=256), d), (g, table(rows=128, cols=256), d)):
+        assert lib.uw_moe_workspace_bytes(*[C.byref(t) for t in bad], 5, 2) == 0
+    assert lib.uw_moe_workspace_bytes(C.byref(g), C.byref(u), C.byref(d), 5, 5) == 0
+
+    def block(gate=g, logits=P, typ=1, k=2, x=P, T=5, y=P, ws=P, n=need):
+        return lib.uw_moe_block(C.byref(gate), C.byref(u), C.byref(d), logits, typ, k, 1, x, T, None, y, ws, n, None)
+
+    for bad in (dict(gate=table(rows=128, cols=256)), dict(logits=None), dict(typ=7), dict(k=0), dict(x=None),
+                dict(x=P + 2), dict(T=-1), dict(y=None), dict(ws=None)):
+        assert block(**bad) == uw.UW_ERR_INVALID_ARG, bad
+    assert block(n=need - 1) == uw.UW_ERR_WORKSPACE_TOO_SMALL
+    assert block(T=0) == uw.UW_OK
+
+
+def test_the_plain_forms_themselves():
+    """The references of the GPU tests at values worked by hand."""
+    assert act_f64([-1.0, 2.0], "relu").tolist() == [0.0, 2.0]
+    assert abs(act_f64([1.0], "gelu")[0] - 0.841344746068543) < 1e-14
+    assert abs(act_f64([1.0], "gelu_tanh")[0] - 0.841191990608276) < 1e-14
+    w, e, s, rows, off = route_ref(np.array([[0.0, 1.0, 1.0], [5.0, -np.inf, np.nan]], np.float32), 2)
+    assert e.tolist() == [[1, 2], [0, -1]] and w.tolist() == [[0.5, 0.5], [1.0, 0.0]]
+    assert s.tolist() == [[1, 2], [0, -1]] and rows.tolist() == [1, 0, 0] and off.tolist() == [0, 1, 2, 3]

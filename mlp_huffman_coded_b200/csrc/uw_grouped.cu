@@ -31,8 +31,10 @@
 //    through the same rings and share the activation tile; both sums stay in
 //    tensor memory and meet in the epilogue, so g and u are never rounded or
 //    stored.
-//  * The rows of x arrive by TMA gather (4 row numbers per copy): the rows
-//    of a group need not be copied next to each other first.
+//  * The rows of x arrive in 16-row TMA boxes, or, where a group's rows are
+//    scattered, by TMA gather (4 row numbers per copy) while groups are small;
+//    the gather takes about 75 cycles per 4 rows, so beyond kGatherCap rows
+//    per tile a small kernel first copies the rows next to each other.
 //  * A tile shared by several CTAs: each writes its FP32 sums to a slot of
 //    its own (a CTA has at most two such tiles, its first and its last) and
 //    takes a ticket; the last adds all of them in CTA order and runs the
@@ -53,12 +55,14 @@ namespace uw {
 
 namespace {
 
-// Warp roles: 0 = weight producer, 1 = activation producer, 2..5 = MMA
-// issuers (warp 2 owns tensor memory), 6..13 = two rebuild groups of 4 warps
-// (group g rebuilds tiles i with i % 2 == g), 14..17 = epilogue.
+// Warp roles: 0 = weight producer, 1 = activation producer, 2..3 = MMA
+// issuers (warp 2 owns tensor memory), 4..11 = two rebuild groups of 4 warps
+// (group g rebuilds tiles i with i % 2 == g), 12..15 = epilogue.  16 warps
+// leave 128 registers a thread: with the rings taking nearly all of shared
+// memory L1 is small, and what 18 warps spilled came back from L2.
 constexpr int kGroups = 2;
-constexpr int kMaxIssuers = 4;
-constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 6, kWarpEpi = kWarpRebuild + 4 * kGroups;
+constexpr int kMaxIssuers = 2;
+constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 4, kWarpEpi = kWarpRebuild + 4 * kGroups;
 constexpr int kThreads = 32 * (kWarpEpi + 4);
 constexpr int kMaxSlots = 16;
 constexpr uint32_t kTmemCols = 512;
@@ -83,6 +87,7 @@ struct GParams {
   uint32_t x_slot_bytes, w_base, w_slot_bytes, sched_off, bar_off, a_col0;
   int vcap;             // verbatim rows staged per record
   int early;            // offsets are not the previous kernel's output
+  int gather;           // x rows by number (TMA gather), else 16-row boxes
   const int32_t* offsets;
   const int32_t* rows;
   const ExpertDesc* table[2];
@@ -200,9 +205,10 @@ struct Ring {
   int slot;
   uint32_t use;
 };
-__device__ __forceinline__ void ring_next(Ring& r, int slots) {
-  if (++r.slot == slots) {
-    r.slot = 0;
+__device__ __forceinline__ void ring_next(Ring& r, int slots, int step = 1) {  // slots: a multiple of step
+  r.slot += step;
+  if (r.slot >= slots) {
+    r.slot -= slots;
     ++r.use;
   }
 }
@@ -262,17 +268,38 @@ __device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
 // ------------------------------- epilogue ------------------------------------
 // FP32 throughout; the only rounding is the store's.  The GELU forms are
 // written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
-__device__ __forceinline__ float activate(float v, int act) {
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
-    case UW_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
-    case UW_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case UW_ACT_GELU_TANH: {
-      const float t = 1.5957691216057308f * (v + 0.044715f * v * v * v);  // 2 sqrt(2 / pi) (...)
-      return v / (1.0f + expf(-t));
-    }
-    case UW_ACT_SILU: return v / (1.0f + expf(-v));
-    default: return v;
+    case UW_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];  // NaN stays
+      break;
+    case UW_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = 0.5f * v[j] * erfcf(-0.70710678118654752f * v[j]);
+      break;
+    case UW_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float t = 1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]);  // 2 sqrt(2 / pi) (...)
+        v[j] = v[j] / (1.0f + expf(-t));
+      }
+      break;
+    case UW_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = v[j] / (1.0f + expf(-v[j]));
+      break;
+    default: break;
   }
+}
+
+// Warp-wide load of 8 consecutive 32-bit columns of the thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
 }
 
 // ------------------------------- the kernel ----------------------------------
@@ -446,22 +473,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
       bool ok = true;
       do {
-        // lane l gathers rows 4 l .. 4 l + 3 of the tile, and 4 (l + 32) ..
-        // past the tile's last row the last one again (never stored)
-        int r[2][4];
-        const int quads = s.ntile >> 2;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        // lane l gathers rows 4 l .. 4 l + 3 of the tile, past the tile's
+        // last row the last one again (never stored)
+        int r[4] = {};
+        const int lanes = p.gather ? s.ntile >> 2 : s.ntile >> 4;
+        if (p.gather) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int i = s.slot0 + min(4 * (lane + 32 * h) + q, s.nvalid - 1);
-            int row = p.rows ? __ldg(p.rows + i) : i;
-            if (row < 0 || row >= p.x_rows) {
+            r[q] = __ldg(p.rows + s.slot0 + min(4 * lane + q, s.nvalid - 1));
+            if (r[q] < 0 || r[q] >= p.x_rows) {
               record_status(p.status, UW_ERR_INVALID_ARG);
-              row = 0;
+              r[q] = 0;
             }
-            r[h][q] = row;
           }
+        }
         for (int kb = s.kb0; kb < s.kb1; ++kb) {
           if (rx.use > 0) ok = warp_wait(&bars->xempty[rx.slot], (rx.use - 1) & 1, bars, p.status);
           if (!ok) break;
@@ -469,9 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(s.ntile) * 128u);
           __syncwarp();
           uint8_t* dst = smem + static_cast<uint32_t>(rx.slot) * p.x_slot_bytes;
-          if (lane < quads) tma_gather4(dst + lane * 512, &tm_x, kb * 64, r[0][0], r[0][1], r[0][2], r[0][3], bar);
-          if (lane + 32 < quads)
-            tma_gather4(dst + (lane + 32) * 512, &tm_x, kb * 64, r[1][0], r[1][1], r[1][2], r[1][3], bar);
+          if (lane < lanes) {
+            if (p.gather) tma_gather4(dst + lane * 512, &tm_x, kb * 64, r[0], r[1], r[2], r[3], bar);
+            else tma_load_2d(dst + lane * 2048, &tm_x, kb * 64, s.slot0 + 16 * lane, bar);
+          }
           ++issued;
           ring_next(rx, p.sx);
         }
@@ -491,11 +517,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && iss < p.n_iss && u0 < u1) {
       Seg s;
       seg_init(s, sched, p, u0, u1);
-      Ring rx{0, 0}, ra{0, 0};
-      int turn = 0;
+      // with two matrices issuer m has matrix m's tile of every k-block; with
+      // one, the issuers take turns
+      const int per = p.n_iss / NMAT, kstep = NMAT * per;
+      const int m = NMAT == 2 ? iss : 0;
+      Ring rx{0, 0}, ra{m, 0};
+      int skip = NMAT == 2 ? 0 : iss;  // k-blocks before this issuer's next
+      if (NMAT == 1) {
+        rx.slot = skip;
+        ra.slot = skip;
+      }
       uint32_t ab = 0, seg = 0;
       bool ok = true;
       const uint64_t x_desc0 = smem_desc_sw128(smem_s);
+      const uint32_t x_step = p.x_slot_bytes >> 4;
       do {
         if (seg >= static_cast<uint32_t>(p.n_acc)) {
           ok = mbar_wait(&bars->acc_empty[ab], (seg / p.n_acc - 1) & 1, &bars->abort, p.status);
@@ -505,30 +540,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = idesc_bf16_f32(s.ntile);
         const uint32_t d = tmem + (ab * p.n_iss + iss) * static_cast<uint32_t>(p.cap);
         uint32_t acc = 0;
-        for (int kb = s.kb0; kb < s.kb1 && ok; ++kb, ring_next(rx, p.sx)) {
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) {
-            if (ok && turn == iss) {
-              ok = mbar_wait(&bars->xfull[rx.slot], rx.use & 1, &bars->abort, p.status) &&
-                   mbar_wait(&bars->afull[ra.slot], ra.use & 1, &bars->abort, p.status);
-              if (ok) {
-                tc_fence_after();
-                const uint32_t a = tmem + p.a_col0 + static_cast<uint32_t>(ra.slot) * 32;
-                const uint64_t b = x_desc0 + static_cast<uint64_t>(static_cast<uint32_t>(rx.slot) * (p.x_slot_bytes >> 4));
-                mma_ts(d, a, b, idesc, acc);
-                mma_ts(d, a + 8, b + 2, idesc, 1u);
-                mma_ts(d, a + 16, b + 4, idesc, 1u);
-                mma_ts(d, a + 24, b + 6, idesc, 1u);
-                acc = 1;
-                tc_commit(&bars->aempty[ra.slot]);
-                tc_commit(&bars->xempty[rx.slot]);
-              }
-            }
-            if (++turn == p.n_iss) turn = 0;
-            ring_next(ra, p.sa);
-          }
+        const int n_kb = s.kb1 - s.kb0;
+        int kb = skip;
+        for (; kb < n_kb; kb += per) {
+          ok = mbar_wait(&bars->xfull[rx.slot], rx.use & 1, &bars->abort, p.status) &&
+               mbar_wait(&bars->afull[ra.slot], ra.use & 1, &bars->abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tmem + p.a_col0 + static_cast<uint32_t>(ra.slot) * 32;
+          const uint64_t b = x_desc0 + static_cast<uint64_t>(static_cast<uint32_t>(rx.slot) * x_step);
+          mma_ts(d, a, b, idesc, acc);
+          mma_ts(d, a + 8, b + 2, idesc, 1u);
+          mma_ts(d, a + 16, b + 4, idesc, 1u);
+          mma_ts(d, a + 24, b + 6, idesc, 1u);
+          acc = 1;
+          tc_commit(&bars->aempty[ra.slot]);
+          tc_commit(&bars->xempty[rx.slot]);
+          ring_next(rx, p.sx, per);
+          ring_next(ra, p.sa, kstep);
         }
         if (!ok) break;
+        skip = kb - n_kb;
         tc_commit(&bars->acc_full[ab]);
         ++seg;
         if (++ab == static_cast<uint32_t>(p.n_acc)) ab = 0;
@@ -541,92 +573,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kWarpEpi) {
     // ------------------------------- rebuild --------------------------------
     // a warp reaches the TMEM lanes 32 (warp % 4) .., so those are its rows
-    const int r = (warp & 3) * 32 + lane;
+    const int w = warp & 3;
+    const int r = w * 32 + lane;
     const int grp = (warp - kWarpRebuild) >> 2;
     if (u0 < u1) {
       Seg s;
       seg_init(s, sched, p, u0, u1);
-      Ring rw{0, 0}, ra{0, 0};
-      int turn = 0;
+      // with two matrices group m has matrix m's tile of every k-block; with
+      // one, the groups take turns
+      constexpr int kStep = NMAT == 2 ? 1 : kGroups;  // k-blocks from one tile of a group to the next
+      Ring rw{grp, 0}, ra{grp, 0};
+      int skip = NMAT == 2 ? 0 : grp;
       bool ok = true;
       PaletteTables pal{};
       bool uniform = true;
-      const uint8_t* tails = nullptr;
-      uint32_t n_verb = 0;
       int cur_e = -1;
-      const uint32_t lanes = tmem + (static_cast<uint32_t>((r >> 5) * 32) << 16) + p.a_col0;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16) + p.a_col0;
       do {
-        for (int kb = s.kb0; kb < s.kb1 && ok; ++kb) {
+        if (cur_e != s.e) {
+          const ExpertDesc* d = desc(NMAT == 2 ? grp : 0, s.e);
+          pal = load_palette(d);
+          uniform = d->mixed == 0;
+          cur_e = s.e;
+        }
+        const int n_kb = s.kb1 - s.kb0;
+        int kb = skip;
+#pragma unroll 1
+        for (; kb < n_kb; kb += kStep) {
+          ok = warp_wait(&bars->wfull[rw.slot], rw.use & 1, bars, p.status);
+          if (!ok) break;
+          const uint32_t body = smem_s + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
+          uint32_t o[32];
+          if (uniform) rebuild_row(pal, true, body, r, o);
+          else rebuild_row(pal, false, body, r, o);
+          // verbatim rows: one mask bit per row, no per-element test
+          const uint4 mk = lds128(body + kBodyMask);
+          const uint32_t mw = w == 0 ? mk.x : (w == 1 ? mk.y : (w == 2 ? mk.z : mk.w));
+          if ((mw >> lane) & 1) {
+            const int idx = (w > 0 ? __popc(mk.x) : 0) + (w > 1 ? __popc(mk.y) : 0) + (w > 2 ? __popc(mk.z) : 0) +
+                            __popc(mw & ((1u << lane) - 1));
+            if (idx < p.vcap) {
 #pragma unroll
-          for (int m = 0; m < NMAT; ++m) {
-            if (ok && turn == grp) {
-              if (cur_e != s.e) {  // with two matrices, a group always has the same one
-                const ExpertDesc* d = desc(m, s.e);
-                pal = load_palette(d);
-                uniform = d->mixed == 0;
-                tails = d->tails;
-                n_verb = d->n_verbatim;
-                cur_e = s.e;
+              for (int c = 0; c < 8; ++c) {
+                const uint4 v = lds128(body + kBody + idx * 128 + 16 * c);
+                o[4 * c] = v.x;
+                o[4 * c + 1] = v.y;
+                o[4 * c + 2] = v.z;
+                o[4 * c + 3] = v.w;
               }
-              ok = warp_wait(&bars->wfull[rw.slot], rw.use & 1, bars, p.status);
-              if (ok) {
-                const uint32_t body = smem_s + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
-                uint32_t o[32];
-                if (uniform) rebuild_row(pal, true, body, r, o);
-                else rebuild_row(pal, false, body, r, o);
-                // verbatim rows: one mask bit per row, no per-element test
-                const uint4 mk = lds128(body + kBodyMask);
-                const int w = r >> 5;
-                const uint32_t mw = w == 0 ? mk.x : (w == 1 ? mk.y : (w == 2 ? mk.z : mk.w));
-                if ((mw >> lane) & 1) {
-                  const int idx = (w > 0 ? __popc(mk.x) : 0) + (w > 1 ? __popc(mk.y) : 0) +
-                                  (w > 2 ? __popc(mk.z) : 0) + __popc(mw & ((1u << lane) - 1));
-                  if (idx < p.vcap) {
+            } else {
+              // more verbatim rows than staged ones: from HBM
+              const ExpertDesc* d = desc(NMAT == 2 ? grp : 0, s.e);
+              const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
+              if (g < d->n_verbatim) {
+                const uint4* src = reinterpret_cast<const uint4*>(d->tails + g * 128u);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                      const uint4 v = lds128(body + kBody + idx * 128 + 16 * c);
-                      o[4 * c] = v.x;
-                      o[4 * c + 1] = v.y;
-                      o[4 * c + 2] = v.z;
-                      o[4 * c + 3] = v.w;
-                    }
-                  } else {
-                    // more verbatim rows than staged ones: from HBM
-                    const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
-                    if (g < n_verb) {
-                      const uint4* src = reinterpret_cast<const uint4*>(tails + g * 128u);
-#pragma unroll
-                      for (int c = 0; c < 8; ++c) {
-                        const uint4 v = __ldg(src + c);
-                        o[4 * c] = v.x;
-                        o[4 * c + 1] = v.y;
-                        o[4 * c + 2] = v.z;
-                        o[4 * c + 3] = v.w;
-                      }
-                    } else {
-                      record_status(p.status, UW_ERR_CORRUPT);
-                    }
-                  }
+                for (int c = 0; c < 8; ++c) {
+                  const uint4 v = __ldg(src + c);
+                  o[4 * c] = v.x;
+                  o[4 * c + 1] = v.y;
+                  o[4 * c + 2] = v.z;
+                  o[4 * c + 3] = v.w;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->wempty[rw.slot]);
-                // the A slot is free once the MMAs of its previous use are done
-                if (ra.use > 0) ok = warp_wait(&bars->aempty[ra.slot], (ra.use - 1) & 1, bars, p.status);
-                if (ok) {
-                  tc_fence_after();
-                  tmem_st32(lanes + static_cast<uint32_t>(ra.slot) * 32, o);
-                  tc_wait_st();
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(&bars->afull[ra.slot]);
-                }
+              } else {
+                record_status(p.status, UW_ERR_CORRUPT);
               }
             }
-            if (++turn == kGroups) turn = 0;
-            ring_next(rw, p.sw);
-            ring_next(ra, p.sa);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->wempty[rw.slot]);
+          // the A slot is free once the MMAs of its previous use are done
+          if (ra.use > 0) {
+            ok = warp_wait(&bars->aempty[ra.slot], (ra.use - 1) & 1, bars, p.status);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          tmem_st32(lanes + static_cast<uint32_t>(ra.slot) * 32, o);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->afull[ra.slot]);
+          ring_next(rw, p.sw, kGroups);
+          ring_next(ra, p.sa, kGroups);
         }
+        skip = kb - n_kb;
       } while (ok && seg_next(s, sched, p));
     }
   } else {
@@ -653,47 +683,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = s.mt * 128 + r;
         const int n_kb = s.kb1 - s.kb0;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap);
-        const int n_chunks = (s.nvalid + 15) >> 4;
-        // this CTA's sums of 16 columns of matrix m: its issuers' sums in
-        // the order of their first k-block (a segment shorter than the
-        // number of issuers leaves some without)
-        auto own_sum = [&](int m, int cc, float (&acc)[16]) {
+        const int n_chunks = (s.nvalid + 7) >> 3;
+        // this CTA's sums of 8 columns of matrix m: its issuers' sums in the
+        // order of their first k-block (a segment shorter than the number of
+        // issuers leaves some without)
+        auto own_sum = [&](int m, int cc, float (&acc)[8]) {
 #pragma unroll 1
           for (int i = 0; i < per && i < n_kb; ++i) {
             const int issuer = (first_tile + i * NMAT + m) % p.n_iss;
-            uint32_t v[16];
-            tmem_ld16(taddr + static_cast<uint32_t>(issuer * p.cap + cc * 16), v);
+            uint32_t v[8];
+            tmem_ld8(taddr + static_cast<uint32_t>(issuer * p.cap + cc * 8), v);
             tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j] = i ? acc[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+            for (int j = 0; j < 8; ++j) acc[j] = i ? acc[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
           }
         };
         const bool row_ok = n < p.N;
         const float bias = p.bias && row_ok ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
                                                   p.bias)[static_cast<int64_t>(s.e) * p.N + n])
                                             : 0.0f;
-        auto emit = [&](const float (&a)[NMAT][16], int cc) {
+        auto emit = [&](float (&a)[NMAT][8], int cc) {
           if (!row_ok) return;
-          const int cols = min(16, s.nvalid - cc * 16);
-          int64_t i = static_cast<int64_t>(s.slot0 + cc * 16) * p.N + n;
+          const int cols = min(8, s.nvalid - cc * 8);
+          int64_t i = static_cast<int64_t>(s.slot0 + cc * 8) * p.N + n;
+          if constexpr (NMAT == 2) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j, i += p.N) {
+            for (int j = 0; j < 8; ++j) a[0][j] = a[0][j] / (1.0f + expf(-a[0][j])) * a[1][j];
+          } else {
+            if (p.bias) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) a[0][j] += bias;
+            }
+            activate(a[0], p.act);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j, i += p.N) {
             if (j >= cols) continue;
             float v = a[0][j];
-            if constexpr (NMAT == 2) {
-              v = v / (1.0f + expf(-v)) * a[1][j];
-            } else {
-              if (p.bias) v += bias;
-              v = activate(v, p.act);
-              if (p.residual) v += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
-            }
+            if (NMAT == 1 && p.residual) v += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
             if (p.out_fp32) static_cast<float*>(p.y)[i] = v;
             else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
           }
         };
         if (n_kb == p.KB) {
+#pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
-            float a[NMAT][16];
+            float a[NMAT][8];
 #pragma unroll
             for (int m = 0; m < NMAT; ++m) own_sum(m, cc, a[m]);
             emit(a, cc);
@@ -707,20 +742,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_last = unit_owner(s.tile_u + p.KB - 1, total, grid);
           const int n_contrib = c_last - c_first + 1;
           // contributor c's sums: its slot 0 when the tile opens its share,
-          // else slot 1; [matrix][chunk][weight row][16 columns]
+          // else slot 1; [matrix][chunk][weight row][8 columns]
           auto part = [&](int c) -> float* {
             const int which = units_before(c, total, grid) >= s.tile_u ? 0 : 1;
             return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
           };
           float* mine = part(cta);
+#pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
 #pragma unroll
             for (int m = 0; m < NMAT; ++m) {
-              float a[16];
+              float a[8];
               own_sum(m, cc, a);
-              float4* dst = reinterpret_cast<float4*>(mine + ((m * n_chunks + cc) * 128 + r) * 16);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) __stcg(dst + k, make_float4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]));
+              float4* dst = reinterpret_cast<float4*>(mine + ((m * n_chunks + cc) * 128 + r) * 8);
+              __stcg(dst, make_float4(a[0], a[1], a[2], a[3]));
+              __stcg(dst + 1, make_float4(a[4], a[5], a[6], a[7]));
             }
           }
           tc_fence_before();
@@ -735,24 +771,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           group_sync();
           if (*last_flag) {
+            const float* first = part(c_first);
+            const float* later = part(c_last) - 2 * p.partial_stride * c_last;  // slot 0 of the others
+#pragma unroll 1
             for (int cc = 0; cc < n_chunks; ++cc) {
-              float a[NMAT][16];
+              float a[NMAT][8];
 #pragma unroll
               for (int m = 0; m < NMAT; ++m) {
-                const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 16;
+                const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 8;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) a[m][j] = 0.0f;
-#pragma unroll 2
+                for (int j = 0; j < 8; ++j) a[m][j] = 0.0f;
+#pragma unroll 4
                 for (int c = c_first; c <= c_last; ++c) {
-                  const float4* src = reinterpret_cast<const float4*>(part(c) + at);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float4 v = __ldcg(src + k);
-                    a[m][4 * k] += v.x;
-                    a[m][4 * k + 1] += v.y;
-                    a[m][4 * k + 2] += v.z;
-                    a[m][4 * k + 3] += v.w;
-                  }
+                  const float4* src =
+                      reinterpret_cast<const float4*>((c == c_first ? first : later + 2 * p.partial_stride * c) + at);
+                  const float4 v0 = __ldcg(src), v1 = __ldcg(src + 1);
+                  a[m][0] += v0.x;
+                  a[m][1] += v0.y;
+                  a[m][2] += v0.z;
+                  a[m][3] += v0.w;
+                  a[m][4] += v1.x;
+                  a[m][5] += v1.y;
+                  a[m][6] += v1.z;
+                  a[m][7] += v1.w;
                 }
               }
               emit(a, cc);
@@ -774,7 +815,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------- rows next to each other ---------------------------
+// out[s] = x[rows[s]] for the slots of all groups: 16-byte pieces.
+struct PermuteParams {
+  const uint4* x;
+  const int32_t* rows;
+  const int32_t* offsets;
+  uint4* out;
+  int E, x_rows, n_rows, pieces;  // pieces of 16 bytes per row
+  uint32_t* status;
+};
+__global__ void __launch_bounds__(256) permute_kernel(const PermuteParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int first = max(0, p.offsets[0]), last = min(p.n_rows, p.offsets[p.E]);
+  for (int s = first + static_cast<int>(blockIdx.x); s < last; s += static_cast<int>(gridDim.x)) {
+    int r = p.rows[s];
+    if (r < 0 || r >= p.x_rows) {
+      if (threadIdx.x == 0) record_status(p.status, UW_ERR_INVALID_ARG);
+      r = 0;
+    }
+    const uint4* src = p.x + static_cast<int64_t>(r) * p.pieces;
+    uint4* dst = p.out + static_cast<int64_t>(s) * p.pieces;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.pieces; i += 256) dst[i] = __ldg(src + i);
+  }
+}
+
 // ------------------------------- host side -----------------------------------
+
+// Rows per tile up to which scattered rows are gathered by TMA.
+constexpr int kGatherCap = 32;
 
 struct GLayout {
   int cap = 16, n_iss = 1, n_acc = 1, sx = 2, sa = 2, sw = 2, vcap = 0;
@@ -838,10 +909,11 @@ struct GPlan {
   GLayout lay;
   int n_mt = 0, KB = 0, grid = 0;
   size_t partial_stride = 0;  // floats
+  size_t permuted = 0;        // offset of the rows laid next to each other, 0: none
   size_t bytes = 0;           // workspace
 };
 
-uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, int sms, GPlan* out) {
+uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, bool scattered, int sms, GPlan* out) {
   if (E < 1 || E > kMaxExperts || n_rows < 0) return UW_ERR_INVALID_ARG;
   if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
   GPlan g;
@@ -855,6 +927,10 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, int sm
   g.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), sms));
   g.partial_stride = static_cast<size_t>(nmat) * 128 * g.lay.cap;
   g.bytes = kWsHeader + kCounterBytes + align_up(2 * static_cast<size_t>(g.grid) * g.partial_stride * 4, 256);
+  if (scattered && g.lay.cap > kGatherCap) {
+    g.permuted = g.bytes;
+    g.bytes += align_up(static_cast<size_t>(n_rows) * K * 2, 256);
+  }
   *out = g;
   return UW_OK;
 }
@@ -881,6 +957,22 @@ uw_status launch_grouped_kernel(const CUtensorMap& tx, const GParams& gp, size_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_kernel<NMAT>, tx, gp);
+  note_launch();
+  if (err != cudaSuccess) return cuda_status(err);
+  return cuda_status(cudaGetLastError());
+}
+
+uw_status launch_permute(const PermuteParams& q, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, permute_kernel, q);
   note_launch();
   if (err != cudaSuccess) return cuda_status(err);
   return cuda_status(cudaGetLastError());
@@ -922,9 +1014,9 @@ uw_status expert_desc(const uw_matrix* m, ExpertDesc* out) {
   return UW_OK;
 }
 
-size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat) {
+size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat, bool scattered) {
   GPlan g;
-  return grouped_plan(N, K, E, n_rows, nmat, sms_or_default(), &g) == UW_OK ? g.bytes : 0;
+  return grouped_plan(N, K, E, n_rows, nmat, scattered, sms_or_default(), &g) == UW_OK ? g.bytes : 0;
 }
 
 uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
@@ -933,7 +1025,7 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   if (st != UW_OK) return st;
   const int nmat = a.swiglu ? 2 : 1;
   GPlan g;
-  if ((st = grouped_plan(a.N, a.K, a.E, a.n_rows, nmat, dev.sm_count, &g)) != UW_OK) return st;
+  if ((st = grouped_plan(a.N, a.K, a.E, a.n_rows, nmat, a.rows != nullptr, dev.sm_count, &g)) != UW_OK) return st;
   if (!a.x || !a.y || !a.ws || !aligned16(a.x) || !aligned16(a.y) || !aligned16(a.ws) || a.x_rows < 1)
     return UW_ERR_INVALID_ARG;
   if (!aligned_to(a.offsets, 4) || !aligned_to(a.rows, 4) || !aligned_to(a.bias, 2) || !aligned_to(a.residual, 2))
@@ -942,9 +1034,28 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
       a.out_type > UW_OUT_FP32)
     return UW_ERR_INVALID_ARG;
   if (a.ws_bytes < g.bytes) return UW_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  const void* x = a.x;
+  int x_rows = a.x_rows;
+  const bool gather = a.rows && !g.permuted;
+  if (g.permuted) {
+    PermuteParams q;
+    q.x = reinterpret_cast<const uint4*>(a.x);
+    q.rows = a.rows;
+    q.offsets = a.offsets;
+    q.out = reinterpret_cast<uint4*>(ws + g.permuted);
+    q.E = a.E;
+    q.x_rows = a.x_rows;
+    q.n_rows = a.n_rows;
+    q.pieces = static_cast<int>(a.K / 8);
+    q.status = reinterpret_cast<uint32_t*>(ws);
+    if ((st = launch_permute(q, std::min(a.n_rows, 8 * dev.sm_count), s)) != UW_OK) return st;
+    x = q.out;
+    x_rows = a.n_rows;
+  }
   CUtensorMap tx;
-  if ((st = make_tensor_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, static_cast<uint64_t>(a.K),
-                               static_cast<uint64_t>(a.x_rows), static_cast<uint64_t>(a.K) * 2, 64, 1,
+  if ((st = make_tensor_map_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, static_cast<uint64_t>(a.K),
+                               static_cast<uint64_t>(x_rows), static_cast<uint64_t>(a.K) * 2, 64, gather ? 1 : 16,
                                CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
     return st;
   GParams p;
@@ -953,8 +1064,9 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   p.N = static_cast<int>(a.N);
   p.KB = g.KB;
   p.n_mt = g.n_mt;
-  p.x_rows = a.x_rows;
+  p.x_rows = x_rows;
   p.n_rows = a.n_rows;
+  p.gather = gather ? 1 : 0;
   p.grid = g.grid;
   p.cap = g.lay.cap;
   p.n_iss = g.lay.n_iss;
@@ -969,7 +1081,9 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   p.bar_off = g.lay.bar_off;
   p.a_col0 = g.lay.a_col0;
   p.vcap = g.lay.vcap;
-  p.early = a.offsets == nullptr || a.offsets_ready;
+  // (the permuting kernel lets this one in after waiting for its own
+  // predecessor, which may have written the offsets)
+  p.early = a.offsets == nullptr || a.offsets_ready || g.permuted;
   p.offsets = a.offsets;
   p.rows = a.rows;
   p.table[0] = static_cast<const ExpertDesc*>(a.table[0]);
@@ -980,7 +1094,6 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   p.act = a.activation;
   p.out_fp32 = a.out_type == UW_OUT_FP32;
   p.y = a.y;
-  uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.status = reinterpret_cast<uint32_t*>(ws);
   p.counters = reinterpret_cast<uint32_t*>(ws + kWsHeader);
   p.partials = reinterpret_cast<float*>(ws + kWsHeader + kCounterBytes);
@@ -1027,7 +1140,7 @@ bool experts_ok(const uw_experts* w) { return w && w->table && aligned16(w->tabl
 }  // namespace
 
 extern "C" size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, int32_t swiglu) {
-  return w ? grouped_ws_bytes(w->rows, w->cols, w->n_experts, n_rows, swiglu ? 2 : 1) : 0;
+  return w ? grouped_ws_bytes(w->rows, w->cols, w->n_experts, n_rows, swiglu ? 2 : 1, true) : 0;
 }
 
 extern "C" uw_status uw_gemm_grouped(const uw_experts* w, const uint16_t* x, int32_t x_rows, const int32_t* rows,
@@ -1084,7 +1197,7 @@ extern "C" uw_status uw_gemm_grouped_swiglu(const uw_experts* gate, const uw_exp
 }
 
 extern "C" size_t uw_gemm_epilogue_workspace_bytes(const uw_layout* L, int32_t batch) {
-  return L ? grouped_ws_bytes(L->rows, L->cols, 1, batch, 1) : 0;
+  return L ? grouped_ws_bytes(L->rows, L->cols, 1, batch, 1, false) : 0;
 }
 
 extern "C" uw_status uw_gemm_epilogue(const uw_matrix* m, const uint16_t* x, int32_t batch, const uw_epilogue* epi,

@@ -31,7 +31,7 @@
 //    through the same rings and share the activation tile; both sums stay in
 //    tensor memory and meet in the epilogue, so g and u are never rounded or
 //    stored.
-//  * The rows of x arrive in 16-row TMA boxes, or, where a group's rows are
+//  * The rows of x arrive in TMA boxes of 64 and 16 rows, or, where a group's rows are
 //    scattered, by TMA gather (4 row numbers per copy) while groups are small;
 //    the gather takes about 75 cycles per 4 rows, so beyond kGatherCap rows
 //    per tile a small kernel first copies the rows next to each other.
@@ -65,6 +65,7 @@ constexpr int kMaxIssuers = 2;
 constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 4, kWarpEpi = kWarpRebuild + 4 * kGroups;
 constexpr int kThreads = 32 * (kWarpEpi + 4);
 constexpr int kMaxSlots = 16;
+constexpr int kWBatch = 4;  // tiles that the weight producer issues at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBody = 12304, kBodyIdx = 8192, kBodyMask = 12288;  // pack record of a tile (uw.h)
 constexpr uint32_t kMinTail = 8;  // verbatim rows staged per tile, at least
@@ -80,7 +81,8 @@ struct SchedEntry {
 };
 
 struct GParams {
-  int E, N, KB, n_mt, x_rows, n_rows;
+  int E, N, KB, x_rows, n_rows;
+  int n_mt, n_mt_all;   // row tiles of the schedule (pairs with PAIR), and of the matrix
   int grid, cap;        // columns per tile, at most
   int n_iss, n_acc;
   int sx, sa, sw;       // ring slots: activations, A tiles (tensor memory), weight records
@@ -205,12 +207,19 @@ struct Ring {
   int slot;
   uint32_t use;
 };
-__device__ __forceinline__ void ring_next(Ring& r, int slots, int step = 1) {  // slots: a multiple of step
+__device__ __forceinline__ void ring_next(Ring& r, int slots, int step = 1) {  // step <= slots
   r.slot += step;
   if (r.slot >= slots) {
     r.slot -= slots;
     ++r.use;
   }
+}
+
+// Row tile of matrix m of the k-block: with PAIR the two "matrices" are two
+// row tiles of one (the last one twice where their number is odd).
+template <bool PAIR>
+__device__ __forceinline__ int row_tile(const GParams& p, int mt, int m) {
+  return PAIR ? min(2 * mt + m, p.n_mt_all - 1) : mt;
 }
 
 // ------------------------------- rebuild -------------------------------------
@@ -303,9 +312,10 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
 }
 
 // ------------------------------- the kernel ----------------------------------
-template <int NMAT>
+template <int NMAT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ GParams p) {
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x64,
+                   const __grid_constant__ GParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t smem_s = smem_u32(smem);
@@ -337,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
   } else if (warp == kWarpX && lane == 0) {
     prefetch_tensormap(&tm_x);
+    if (!p.gather) prefetch_tensormap(&tm_x64);
   } else if (warp == kWarpMma) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -395,8 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpW) {
     // --------------------------- weight producer ----------------------------
-    // Lanes hold the verbatim offsets of the next 31 tiles; lane 0 issues a
-    // tile's record and its verbatim rows (one contiguous run).
+    // One lane per tile, kWBatch tiles at a time: each waits for its slot,
+    // then issues its record and its verbatim rows (one contiguous run).  One
+    // thread alone took about 650 cycles per tile, more than HBM needs for
+    // one (530).  The lanes hold the verbatim offsets of the next 31 k-blocks.
+    constexpr int kSpan = 28;  // k-blocks per set of offsets: whole batches, and one offset more
     if (u0 < u1) {
       const uint64_t once = l2_evict_first();
       Seg s;
@@ -404,56 +418,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring rw{0, 0};
       int issued = 0;
       bool ok = true;
+      const int m = NMAT == 2 ? lane & 1 : 0;  // this lane's matrix
       do {
-        const uint8_t *pack[NMAT] = {}, *tails[NMAT] = {};
-        const uint32_t* off[NMAT] = {};
-        uint32_t n_verb[NMAT] = {}, v[NMAT] = {};
-        const int64_t t0 = static_cast<int64_t>(s.mt) * p.KB;
         // lane l: offset of tile kb + l
-        auto fetch = [&](int m, int kb) -> uint32_t {
-          return kb + lane <= s.kb1 ? __ldg(off[m] + t0 + kb + lane) : 0u;
-        };
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m) {
-          const ExpertDesc* d = desc(m, s.e);
-          pack[m] = d->pack;
-          tails[m] = d->tails;
-          off[m] = d->pack_off;
-          n_verb[m] = d->n_verbatim;
-          v[m] = fetch(m, s.kb0);
-        }
+        const ExpertDesc* d0 = desc(0, s.e);
+        const ExpertDesc* d1 = NMAT == 2 && !PAIR ? desc(1, s.e) : d0;
+        const int64_t t0 = static_cast<int64_t>(row_tile<PAIR>(p, s.mt, 0)) * p.KB;
+        const int64_t t1 = static_cast<int64_t>(row_tile<PAIR>(p, s.mt, 1)) * p.KB;
+        const uint32_t* off0 = d0->pack_off + t0 + lane;
+        const uint32_t* off1 = d1->pack_off + t1 + lane;
+        const int last = s.kb1 - lane;
+        uint32_t v0 = s.kb0 <= last ? __ldg(off0 + s.kb0) : 0u;
+        uint32_t v1 = NMAT == 2 && s.kb0 <= last ? __ldg(off1 + s.kb0) : 0u;
+        const ExpertDesc* d = m ? d1 : d0;
+        const uint8_t* pack = d->pack + static_cast<uint64_t>(m ? t1 : t0) * kBody;
+        const uint8_t* tails = d->tails;
+        const uint32_t n_verb = d->n_verbatim;
         // weights that a later column tile reads again stay in L2
         const bool reread = (sched[s.e].n_nt >> 16) > 1;
-        for (int kb = s.kb0; kb < s.kb1 && ok; kb += 31) {
-          uint32_t nv[NMAT];
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) nv[m] = fetch(m, kb + 31);
-          const int n = min(31, s.kb1 - kb);
-          for (int j = 0; j < n && ok; ++j) {
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m) {
-              const uint32_t a = __shfl_sync(0xFFFFFFFFu, v[m], j), b = __shfl_sync(0xFFFFFFFFu, v[m], j + 1);
-              if (ok && rw.use > 0) ok = warp_wait(&bars->wempty[rw.slot], (rw.use - 1) & 1, bars, p.status);
-              if (!ok) continue;
-              if (lane == 0) {
-                uint32_t rows = 0;
-                if (b < a || b - a > 128u || b > n_verb[m]) record_status(p.status, UW_ERR_CORRUPT);
-                else rows = min(b - a, static_cast<uint32_t>(p.vcap));
-                uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
-                uint64_t* bar = &bars->wfull[rw.slot];
-                bars->tail_first[rw.slot] = a;
-                mbar_arrive_expect_tx(bar, kBody + rows * 128u);
-                const uint8_t* src = pack[m] + static_cast<uint64_t>(t0 + kb + j) * kBody;
-                if (reread) bulk_load(slot, src, kBody, bar);
-                else bulk_load_hint(slot, src, kBody, bar, once);
-                if (rows) bulk_load(slot + kBody, tails[m] + static_cast<uint64_t>(a) * 128u, rows * 128u, bar);
+        for (int kb = s.kb0; kb < s.kb1 && ok; kb += kSpan) {
+          const uint32_t w0 = kb + kSpan <= last ? __ldg(off0 + kb + kSpan) : 0u;
+          const uint32_t w1 = NMAT == 2 && kb + kSpan <= last ? __ldg(off1 + kb + kSpan) : 0u;
+          const int n = min(kSpan, s.kb1 - kb) * NMAT;
+          for (int i0 = 0; i0 < n; i0 += kWBatch) {
+            const int j = (i0 + lane) / NMAT;  // k-block of this lane's tile
+            uint32_t a = __shfl_sync(0xFFFFFFFFu, v0, j & 31), b = __shfl_sync(0xFFFFFFFFu, v0, (j + 1) & 31);
+            if constexpr (NMAT == 2) {
+              const uint32_t a1 = __shfl_sync(0xFFFFFFFFu, v1, j & 31), b1 = __shfl_sync(0xFFFFFFFFu, v1, (j + 1) & 31);
+              if (m) {
+                a = a1;
+                b = b1;
               }
-              ++issued;
-              ring_next(rw, p.sw);
             }
+            const int count = min(kWBatch, n - i0);
+            Ring mine = rw;
+            ring_next(mine, p.sw, lane & (kWBatch - 1));
+            bool good = true;
+            if (lane < count && mine.use > 0)
+              good = mbar_wait(&bars->wempty[mine.slot], (mine.use - 1) & 1, &bars->abort, p.status);
+            ok = __all_sync(0xFFFFFFFFu, good);
+            if (!ok) break;
+            if (lane < count) {
+              uint32_t rows = 0;
+              if (b < a || b - a > 128u || b > n_verb) record_status(p.status, UW_ERR_CORRUPT);
+              else rows = min(b - a, static_cast<uint32_t>(p.vcap));
+              uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(mine.slot) * p.w_slot_bytes;
+              uint64_t* bar = &bars->wfull[mine.slot];
+              bars->tail_first[mine.slot] = a;
+              mbar_arrive_expect_tx(bar, kBody + rows * 128u);
+              const uint8_t* src = pack + static_cast<uint64_t>(kb + j) * kBody;
+              if (reread) bulk_load(slot, src, kBody, bar);
+              else bulk_load_hint(slot, src, kBody, bar, once);
+              if (rows) bulk_load(slot + kBody, tails + static_cast<uint64_t>(a) * 128u, rows * 128u, bar);
+            }
+            __syncwarp();
+            issued += count;
+            ring_next(rw, p.sw, count);
           }
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) v[m] = nv[m];
+          v0 = w0;
+          v1 = w1;
         }
       } while (ok && seg_next(s, sched, p));
       // every issued copy lands before the CTA exits (already so unless a
@@ -476,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane l gathers rows 4 l .. 4 l + 3 of the tile, past the tile's
         // last row the last one again (never stored)
         int r[4] = {};
-        const int lanes = p.gather ? s.ntile >> 2 : s.ntile >> 4;
+        // rows in boxes of 64, the rest in boxes of 16: lane l issues one
+        const int big = s.ntile >> 6;
+        const int lanes = p.gather ? s.ntile >> 2 : big + ((s.ntile & 63) >> 4);
+        const int row = lane < big ? 64 * lane : 64 * big + 16 * (lane - big);
         if (p.gather) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -496,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = smem + static_cast<uint32_t>(rx.slot) * p.x_slot_bytes;
           if (lane < lanes) {
             if (p.gather) tma_gather4(dst + lane * 512, &tm_x, kb * 64, r[0], r[1], r[2], r[3], bar);
-            else tma_load_2d(dst + lane * 2048, &tm_x, kb * 64, s.slot0 + 16 * lane, bar);
+            else if (lane < big) tma_load_2d(dst + row * 128, &tm_x64, kb * 64, s.slot0 + row, bar);
+            else tma_load_2d(dst + row * 128, &tm_x, kb * 64, s.slot0 + row, bar);
           }
           ++issued;
           ring_next(rx, p.sx);
@@ -591,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16) + p.a_col0;
       do {
         if (cur_e != s.e) {
-          const ExpertDesc* d = desc(NMAT == 2 ? grp : 0, s.e);
+          const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp : 0, s.e);
           pal = load_palette(d);
           uniform = d->mixed == 0;
           cur_e = s.e;
@@ -623,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               // more verbatim rows than staged ones: from HBM
-              const ExpertDesc* d = desc(NMAT == 2 ? grp : 0, s.e);
+              const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp : 0, s.e);
               const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
               if (g < d->n_verbatim) {
                 const uint4* src = reinterpret_cast<const uint4*>(d->tails + g * 128u);
@@ -680,7 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[ab], (seg / p.n_acc) & 1, &bars->abort, p.status));
         if (!group_and(ok)) break;
         tc_fence_after();
-        const int n = s.mt * 128 + r;
         const int n_kb = s.kb1 - s.kb0;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap);
         const int n_chunks = (s.nvalid + 7) >> 3;
@@ -698,31 +724,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) acc[j] = i ? acc[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
           }
         };
-        const bool row_ok = n < p.N;
-        const float bias = p.bias && row_ok ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
-                                                  p.bias)[static_cast<int64_t>(s.e) * p.N + n])
-                                            : 0.0f;
-        auto emit = [&](float (&a)[NMAT][8], int cc) {
-          if (!row_ok) return;
+        // values of matrix row n: bias, activation, residual, store
+        auto store8 = [&](float (&v)[8], int cc, int n, float bias) {
+          if (n >= p.N) return;
           const int cols = min(8, s.nvalid - cc * 8);
           int64_t i = static_cast<int64_t>(s.slot0 + cc * 8) * p.N + n;
-          if constexpr (NMAT == 2) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[0][j] = a[0][j] / (1.0f + expf(-a[0][j])) * a[1][j];
-          } else {
+          if (NMAT == 1 || PAIR) {
             if (p.bias) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) a[0][j] += bias;
+              for (int j = 0; j < 8; ++j) v[j] += bias;
             }
-            activate(a[0], p.act);
+            activate(v, p.act);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j, i += p.N) {
             if (j >= cols) continue;
-            float v = a[0][j];
-            if (NMAT == 1 && p.residual) v += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
-            if (p.out_fp32) static_cast<float*>(p.y)[i] = v;
-            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
+            if ((NMAT == 1 || PAIR) && p.residual)
+              v[j] += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
+            if (p.out_fp32) static_cast<float*>(p.y)[i] = v[j];
+            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v[j]);
+          }
+        };
+        int n[NMAT];
+        float bias[NMAT];
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m) {
+          // (unclamped: the second half of an odd last pair is past p.N)
+          n[m] = (PAIR ? 2 * s.mt + m : s.mt) * 128 + r;
+          bias[m] = p.bias && n[m] < p.N ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
+                                               p.bias)[static_cast<int64_t>(s.e) * p.N + n[m]])
+                                         : 0.0f;
+        }
+        auto emit = [&](float (&a)[NMAT][8], int cc) {
+          if constexpr (NMAT == 2 && !PAIR) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[0][j] = a[0][j] / (1.0f + expf(-a[0][j])) * a[1][j];
+            store8(a[0], cc, n[0], 0.0f);
+          } else {
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m) store8(a[m], cc, n[m], bias[m]);
           }
         };
         if (n_kb == p.KB) {
@@ -846,6 +886,8 @@ __global__ void __launch_bounds__(256) permute_kernel(const PermuteParams p) {
 
 // Rows per tile up to which scattered rows are gathered by TMA.
 constexpr int kGatherCap = 32;
+// Columns per tile above which two row tiles share the activation tile.
+constexpr int kPairCap = 64;
 
 struct GLayout {
   int cap = 16, n_iss = 1, n_acc = 1, sx = 2, sa = 2, sw = 2, vcap = 0;
@@ -893,7 +935,7 @@ bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
   const uint32_t w_room = room - static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
   l.sw = std::min(kMaxSlots, static_cast<int>(w_room / (kBody + kMinTail * 128u)));
   l.sw -= l.sw % kGroups;
-  if (l.sw < kGroups || l.sx < 1) return false;
+  if (l.sw < kWBatch || l.sx < 1) return false;
   l.vcap = static_cast<int>(std::min(128u, (w_room / static_cast<uint32_t>(l.sw) - kBody) / 128u));
   l.w_slot_bytes = kBody + static_cast<uint32_t>(l.vcap) * 128u;  // a multiple of 16
   l.w_base = static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
@@ -908,17 +950,22 @@ bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
 struct GPlan {
   GLayout lay;
   int n_mt = 0, KB = 0, grid = 0;
+  bool pair = false;
   size_t partial_stride = 0;  // floats
   size_t permuted = 0;        // offset of the rows laid next to each other, 0: none
   size_t bytes = 0;           // workspace
 };
 
-uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, bool scattered, int sms, GPlan* out) {
+uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, bool scattered, int sms, GPlan* out) {
   if (E < 1 || E > kMaxExperts || n_rows < 0) return UW_ERR_INVALID_ARG;
   if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
   GPlan g;
-  if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
   g.n_mt = static_cast<int>((N + 127) / 128);
+  // large groups: two row tiles share each activation tile
+  g.pair = !swiglu && N > 128 && pick_cap(std::max(n_rows, 1), E, 1) > kPairCap;
+  const int nmat = swiglu || g.pair ? 2 : 1;
+  if (g.pair) g.n_mt = (g.n_mt + 1) / 2;
+  if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
   g.KB = static_cast<int>(K / 64);
   // the most units any split of n_rows into E groups can give
   const int64_t tiles = std::min<int64_t>(n_rows, n_rows / g.lay.cap + E);
@@ -935,14 +982,15 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, int nmat, bool s
   return UW_OK;
 }
 
-template <int NMAT>
-uw_status launch_grouped_kernel(const CUtensorMap& tx, const GParams& gp, size_t smem, cudaStream_t s) {
+template <int NMAT, bool PAIR>
+uw_status launch_grouped_kernel(const CUtensorMap& tx, const CUtensorMap& tx64, const GParams& gp, size_t smem,
+                                cudaStream_t s) {
   static std::once_flag once[64];
   static cudaError_t attr_err[64];
   int dev = 0;
   cudaGetDevice(&dev);
   std::call_once(once[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(grouped_kernel<NMAT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr_err[dev & 63] = cudaFuncSetAttribute(grouped_kernel<NMAT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               static_cast<int>(kSmemLimit));
   });
   if (attr_err[dev & 63] != cudaSuccess) return UW_ERR_CUDA;
@@ -956,7 +1004,7 @@ uw_status launch_grouped_kernel(const CUtensorMap& tx, const GParams& gp, size_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_kernel<NMAT>, tx, gp);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, grouped_kernel<NMAT, PAIR>, tx, tx64, gp);
   note_launch();
   if (err != cudaSuccess) return cuda_status(err);
   return cuda_status(cudaGetLastError());
@@ -1014,18 +1062,17 @@ uw_status expert_desc(const uw_matrix* m, ExpertDesc* out) {
   return UW_OK;
 }
 
-size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat, bool scattered) {
+size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, bool swiglu, bool scattered) {
   GPlan g;
-  return grouped_plan(N, K, E, n_rows, nmat, scattered, sms_or_default(), &g) == UW_OK ? g.bytes : 0;
+  return grouped_plan(N, K, E, n_rows, swiglu, scattered, sms_or_default(), &g) == UW_OK ? g.bytes : 0;
 }
 
 uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   DeviceInfo dev;
   uw_status st = device_info(&dev);
   if (st != UW_OK) return st;
-  const int nmat = a.swiglu ? 2 : 1;
   GPlan g;
-  if ((st = grouped_plan(a.N, a.K, a.E, a.n_rows, nmat, a.rows != nullptr, dev.sm_count, &g)) != UW_OK) return st;
+  if ((st = grouped_plan(a.N, a.K, a.E, a.n_rows, a.swiglu, a.rows != nullptr, dev.sm_count, &g)) != UW_OK) return st;
   if (!a.x || !a.y || !a.ws || !aligned16(a.x) || !aligned16(a.y) || !aligned16(a.ws) || a.x_rows < 1)
     return UW_ERR_INVALID_ARG;
   if (!aligned_to(a.offsets, 4) || !aligned_to(a.rows, 4) || !aligned_to(a.bias, 2) || !aligned_to(a.residual, 2))
@@ -1058,12 +1105,18 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
                                static_cast<uint64_t>(x_rows), static_cast<uint64_t>(a.K) * 2, 64, gather ? 1 : 16,
                                CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
     return st;
+  CUtensorMap tx64 = tx;
+  if (!gather && (st = make_tensor_map_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, static_cast<uint64_t>(a.K),
+                                          static_cast<uint64_t>(x_rows), static_cast<uint64_t>(a.K) * 2, 64, 64,
+                                          CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
+    return st;
   GParams p;
   std::memset(&p, 0, sizeof(p));
   p.E = a.E;
   p.N = static_cast<int>(a.N);
   p.KB = g.KB;
   p.n_mt = g.n_mt;
+  p.n_mt_all = static_cast<int>((a.N + 127) / 128);
   p.x_rows = x_rows;
   p.n_rows = a.n_rows;
   p.gather = gather ? 1 : 0;
@@ -1098,7 +1151,9 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   p.counters = reinterpret_cast<uint32_t*>(ws + kWsHeader);
   p.partials = reinterpret_cast<float*>(ws + kWsHeader + kCounterBytes);
   p.partial_stride = static_cast<long long>(g.partial_stride);
-  return nmat == 2 ? launch_grouped_kernel<2>(tx, p, g.lay.smem, s) : launch_grouped_kernel<1>(tx, p, g.lay.smem, s);
+  if (a.swiglu) return launch_grouped_kernel<2, false>(tx, tx64, p, g.lay.smem, s);
+  return g.pair ? launch_grouped_kernel<2, true>(tx, tx64, p, g.lay.smem, s)
+                : launch_grouped_kernel<1, false>(tx, tx64, p, g.lay.smem, s);
 }
 
 }  // namespace uw
@@ -1140,7 +1195,7 @@ bool experts_ok(const uw_experts* w) { return w && w->table && aligned16(w->tabl
 }  // namespace
 
 extern "C" size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, int32_t swiglu) {
-  return w ? grouped_ws_bytes(w->rows, w->cols, w->n_experts, n_rows, swiglu ? 2 : 1, true) : 0;
+  return w ? grouped_ws_bytes(w->rows, w->cols, w->n_experts, n_rows, swiglu != 0, true) : 0;
 }
 
 extern "C" uw_status uw_gemm_grouped(const uw_experts* w, const uint16_t* x, int32_t x_rows, const int32_t* rows,
@@ -1197,7 +1252,7 @@ extern "C" uw_status uw_gemm_grouped_swiglu(const uw_experts* gate, const uw_exp
 }
 
 extern "C" size_t uw_gemm_epilogue_workspace_bytes(const uw_layout* L, int32_t batch) {
-  return L ? grouped_ws_bytes(L->rows, L->cols, 1, batch, 1, false) : 0;
+  return L ? grouped_ws_bytes(L->rows, L->cols, 1, batch, false, false) : 0;
 }
 
 extern "C" uw_status uw_gemm_epilogue(const uw_matrix* m, const uint16_t* x, int32_t batch, const uw_epilogue* epi,

@@ -143,7 +143,7 @@ struct GroupedArgs {
   size_t ws_bytes = 0;
 };
 // `scattered`: room for x's rows next to each other too.  0: unsupported
-size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, int nmat, bool scattered);
+size_t grouped_ws_bytes(int64_t N, int64_t K, int E, int n_rows, bool swiglu, bool scattered);
 uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s);
 
 }  // namespace uw

@@ -475,8 +475,8 @@ bool moe_ws(const uw_experts* gate, const uw_experts* up, const uw_experts* down
   if (!route_plan(T, gate->n_experts, k, &r)) return false;
   const int64_t n = T * k;
   if (n > UW_MAX_SLOTS) return false;
-  const size_t a = grouped_ws_bytes(gate->rows, gate->cols, gate->n_experts, static_cast<int>(n), 2, true);
-  const size_t b = grouped_ws_bytes(down->rows, down->cols, gate->n_experts, static_cast<int>(n), 1, false);
+  const size_t a = grouped_ws_bytes(gate->rows, gate->cols, gate->n_experts, static_cast<int>(n), true, true);
+  const size_t b = grouped_ws_bytes(down->rows, down->cols, gate->n_experts, static_cast<int>(n), false, false);
   if (!a || !b) return false;
   MoeWs w;
   size_t at = align_up(std::max({a, b, r.bytes}), 256);

@@ -56,11 +56,9 @@ namespace uw {
 namespace {
 
 // Warp roles: 0 = weight producer, 1 = activation producer, 2..3 = MMA
-// issuers (warp 2 owns tensor memory), 4..11 = two rebuild groups of 4 warps
-// (group g rebuilds tiles i with i % 2 == g), 12..15 = epilogue.  16 warps
-// leave 128 registers a thread: with the rings taking nearly all of shared
-// memory L1 is small, and what 18 warps spilled came back from L2.
-constexpr int kGroups = 2;
+// issuers (warp 2 owns tensor memory), 4..19 = four rebuild groups of 4 warps
+// (group g rebuilds tiles i with i % 4 == g), 20..23 = epilogue.
+constexpr int kGroups = 4;
 constexpr int kMaxIssuers = 2;
 constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 4, kWarpEpi = kWarpRebuild + 4 * kGroups;
 constexpr int kThreads = 32 * (kWarpEpi + 4);
@@ -86,7 +84,8 @@ struct GParams {
   int grid, cap;        // columns per tile, at most
   int n_iss, n_acc;
   int sx, sa, sw;       // ring slots: activations, A tiles (tensor memory), weight records
-  uint32_t x_slot_bytes, w_base, w_slot_bytes, sched_off, bar_off, a_col0;
+  uint32_t x_slot_bytes, w_base, w_slot_bytes, sched_off, turn_off, bar_off, a_col0;
+  int vec;              // rows of y and the residual start on 16 bytes
   int vcap;             // verbatim rows staged per record
   int early;            // offsets are not the previous kernel's output
   int gather;           // x rows by number (TMA gather), else 16-row boxes
@@ -277,6 +276,12 @@ __device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
 // ------------------------------- epilogue ------------------------------------
 // FP32 throughout; the only rounding is the store's.  The GELU forms are
 // written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
+// SiLU(v) for a product that is rounded to BF16 next: the fast exponential
+// (relative error about 2^-24 (2 + 1.2 |v|), far below BF16's 2^-9 wherever
+// the result is not negligible) and the fast division (2 units in the last
+// place; 0 where exp(-v) overflows, as the limit is).
+__device__ __forceinline__ float silu_fast(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
@@ -606,11 +611,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u0 < u1) {
       Seg s;
       seg_init(s, sched, p, u0, u1);
-      // with two matrices group m has matrix m's tile of every k-block; with
-      // one, the groups take turns
-      constexpr int kStep = NMAT == 2 ? 1 : kGroups;  // k-blocks from one tile of a group to the next
+      // the groups take turns; with two matrices a group's tiles are all of
+      // one (kGroups is even)
+      constexpr int kStep = kGroups / NMAT;  // k-blocks from one tile of a group to the next
       Ring rw{grp, 0}, ra{grp, 0};
-      int skip = NMAT == 2 ? 0 : grp;
+      int skip = grp / NMAT;
       bool ok = true;
       PaletteTables pal{};
       bool uniform = true;
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16) + p.a_col0;
       do {
         if (cur_e != s.e) {
-          const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp : 0, s.e);
+          const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
           pal = load_palette(d);
           uniform = d->mixed == 0;
           cur_e = s.e;
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               // more verbatim rows than staged ones: from HBM
-              const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp : 0, s.e);
+              const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
               const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
               if (g < d->n_verbatim) {
                 const uint4* src = reinterpret_cast<const uint4*>(d->tails + g * 128u);
@@ -701,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       seg_init(s, sched, p, u0, u1);
       uint32_t seg = 0;
       int first_tile = 0;  // the segment's first tile in the CTA's sequence
-      const int per = p.n_iss / NMAT;  // issuers per matrix
+      float* turn = reinterpret_cast<float*>(smem + p.turn_off) + w * 256;
       do {
         const uint32_t ab = seg % p.n_acc;
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[ab], (seg / p.n_acc) & 1, &bars->abort, p.status));
@@ -710,25 +715,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_kb = s.kb1 - s.kb0;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap);
         const int n_chunks = (s.nvalid + 7) >> 3;
-        // this CTA's sums of 8 columns of matrix m: its issuers' sums in the
-        // order of their first k-block (a segment shorter than the number of
-        // issuers leaves some without)
-        auto own_sum = [&](int m, int cc, float (&acc)[8]) {
-#pragma unroll 1
-          for (int i = 0; i < per && i < n_kb; ++i) {
-            const int issuer = (first_tile + i * NMAT + m) % p.n_iss;
-            uint32_t v[8];
-            tmem_ld8(taddr + static_cast<uint32_t>(issuer * p.cap + cc * 8), v);
-            tc_wait_ld();
+        // this CTA's sums of 8 columns, per matrix.  With one matrix and two
+        // issuers: the issuers' sums in the order of their first k-block (a
+        // segment of one k-block has only one)
+        auto own_sums = [&](int cc, float (&a)[NMAT][8]) {
+          uint32_t v[2][8];
+          const uint32_t at = taddr + static_cast<uint32_t>(cc * 8);
+          if constexpr (NMAT == 2) {
+            tmem_ld8(at, v[0]);
+            tmem_ld8(at + p.cap, v[1]);
+          } else {
+            const uint32_t i0 = static_cast<uint32_t>(first_tile % p.n_iss);
+            tmem_ld8(at + i0 * p.cap, v[0]);
+            if (p.n_iss == 2 && n_kb > 1) tmem_ld8(at + (i0 ^ 1u) * p.cap, v[1]);
+          }
+          tc_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = i ? acc[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+          for (int j = 0; j < 8; ++j) {
+            a[0][j] = __uint_as_float(v[0][j]);
+            if constexpr (NMAT == 2) a[NMAT - 1][j] = __uint_as_float(v[1][j]);
+            else if (p.n_iss == 2 && n_kb > 1) a[0][j] += __uint_as_float(v[1][j]);
           }
         };
-        // values of matrix row n: bias, activation, residual, store
+        // values of matrix row n, 8 slots: bias, activation, residual, store.
+        // Where rows of y start on 16 bytes the warp turns its 32 x 8 values
+        // around in shared memory, so that a lane stores 8 consecutive ones
         auto store8 = [&](float (&v)[8], int cc, int n, float bias) {
-          if (n >= p.N) return;
-          const int cols = min(8, s.nvalid - cc * 8);
-          int64_t i = static_cast<int64_t>(s.slot0 + cc * 8) * p.N + n;
           if (NMAT == 1 || PAIR) {
             if (p.bias) {
 #pragma unroll
@@ -736,13 +748,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             activate(v, p.act);
           }
+          const int cols = s.nvalid - cc * 8;
+          if (p.vec) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j, i += p.N) {
-            if (j >= cols) continue;
+            for (int j = 0; j < 8; ++j) turn[j * 32 + lane] = v[j];
+            __syncwarp();
+            const float4 q0 = *reinterpret_cast<const float4*>(turn + lane * 8);
+            const float4 q1 = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
+            __syncwarp();
+            const int n0 = n - lane + (lane & 3) * 8;  // lane l: slot l / 4, rows 8 (l % 4) ..
+            if ((lane >> 2) >= cols || n0 >= p.N) return;
+            float f[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+            const int64_t i = static_cast<int64_t>(s.slot0 + cc * 8 + (lane >> 2)) * p.N + n0;
+            if ((NMAT == 1 || PAIR) && p.residual) {
+              const uint4 u = *reinterpret_cast<const uint4*>(p.residual + i);
+              const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                f[2 * j] += __uint_as_float(w4[j] << 16);
+                f[2 * j + 1] += __uint_as_float(w4[j] & 0xFFFF0000u);
+              }
+            }
+            if (p.out_fp32) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.y) + i);
+              dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+              dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                o[j] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + i) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            return;
+          }
+          if (n >= p.N) return;
+          int64_t i = static_cast<int64_t>(s.slot0 + cc * 8) * p.N + n;
+#pragma unroll 1
+          for (int j = 0; j < 8 && j < cols; ++j, i += p.N) {
+            float f = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) f = j == q ? v[q] : f;
             if ((NMAT == 1 || PAIR) && p.residual)
-              v[j] += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
-            if (p.out_fp32) static_cast<float*>(p.y)[i] = v[j];
-            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v[j]);
+              f += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
+            if (p.out_fp32) static_cast<float*>(p.y)[i] = f;
+            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(f);
           }
         };
         int n[NMAT];
@@ -758,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto emit = [&](float (&a)[NMAT][8], int cc) {
           if constexpr (NMAT == 2 && !PAIR) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[0][j] = a[0][j] / (1.0f + expf(-a[0][j])) * a[1][j];
+            for (int j = 0; j < 8; ++j) a[0][j] = silu_fast(a[0][j]) * a[1][j];
             store8(a[0], cc, n[0], 0.0f);
           } else {
 #pragma unroll
@@ -769,8 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
             float a[NMAT][8];
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m) own_sum(m, cc, a[m]);
+            own_sums(cc, a);
             emit(a, cc);
           }
           tc_fence_before();
@@ -790,13 +841,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* mine = part(cta);
 #pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
+            float a[NMAT][8];
+            own_sums(cc, a);
 #pragma unroll
             for (int m = 0; m < NMAT; ++m) {
-              float a[8];
-              own_sum(m, cc, a);
               float4* dst = reinterpret_cast<float4*>(mine + ((m * n_chunks + cc) * 128 + r) * 8);
-              __stcg(dst, make_float4(a[0], a[1], a[2], a[3]));
-              __stcg(dst + 1, make_float4(a[4], a[5], a[6], a[7]));
+              __stcg(dst, make_float4(a[m][0], a[m][1], a[m][2], a[m][3]));
+              __stcg(dst + 1, make_float4(a[m][4], a[m][5], a[m][6], a[m][7]));
             }
           }
           tc_fence_before();
@@ -891,7 +942,7 @@ constexpr int kPairCap = 64;
 
 struct GLayout {
   int cap = 16, n_iss = 1, n_acc = 1, sx = 2, sa = 2, sw = 2, vcap = 0;
-  uint32_t x_slot_bytes = 0, w_base = 0, w_slot_bytes = 0, sched_off = 0, bar_off = 0, a_col0 = 0;
+  uint32_t x_slot_bytes = 0, w_base = 0, w_slot_bytes = 0, sched_off = 0, turn_off = 0, bar_off = 0, a_col0 = 0;
   size_t smem = 0;
 };
 
@@ -927,7 +978,8 @@ bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
   l.sa -= l.sa % step_a;
   l.x_slot_bytes = static_cast<uint32_t>(l.cap) * 128;
   const uint32_t sched_bytes = (static_cast<uint32_t>(E + 1) * sizeof(SchedEntry) + 127u) & ~127u;
-  const uint32_t fixed = sched_bytes + ((sizeof(GBars) + 127u) & ~127u) + 128u + 1024u;
+  const uint32_t turn_bytes = 4 * 32 * 8 * 4;  // the epilogue warps' values
+  const uint32_t fixed = sched_bytes + turn_bytes + ((sizeof(GBars) + 127u) & ~127u) + 128u + 1024u;
   if (l.sa < step_a || fixed >= kSmemLimit / 2) return false;
   const uint32_t room = static_cast<uint32_t>(kSmemLimit) - fixed;
   l.sx = l.cap <= 32 ? 8 : (l.cap <= 64 ? 6 : (l.cap <= 128 ? 4 : 3));
@@ -940,7 +992,8 @@ bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
   l.w_slot_bytes = kBody + static_cast<uint32_t>(l.vcap) * 128u;  // a multiple of 16
   l.w_base = static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
   l.sched_off = (l.w_base + static_cast<uint32_t>(l.sw) * l.w_slot_bytes + 127u) & ~127u;
-  l.bar_off = l.sched_off + sched_bytes;
+  l.turn_off = l.sched_off + sched_bytes;
+  l.bar_off = l.turn_off + turn_bytes;
   l.smem = std::max<size_t>(l.bar_off + ((sizeof(GBars) + 127u) & ~127u) + 1024u, kSmemFloor);
   if (l.smem > kSmemLimit) return false;
   *out = l;
@@ -1131,6 +1184,8 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   p.w_base = g.lay.w_base;
   p.w_slot_bytes = g.lay.w_slot_bytes;
   p.sched_off = g.lay.sched_off;
+  p.turn_off = g.lay.turn_off;
+  p.vec = a.N % 8 == 0 && aligned16(a.residual);
   p.bar_off = g.lay.bar_off;
   p.a_col0 = g.lay.a_col0;
   p.vcap = g.lay.vcap;

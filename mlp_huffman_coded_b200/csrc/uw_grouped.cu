@@ -118,6 +118,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+// One lane of the warp, the same every time (a converged warp elects alike).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars* b, uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, &b->abort, status));
 }
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t smem_s = smem_u32(smem);
   GBars* bars = reinterpret_cast<GBars*>(smem + p.bar_off);
   SchedEntry* sched = reinterpret_cast<SchedEntry*>(smem + p.sched_off);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
   // ---- set-up: barriers, tensor memory and the table of units
@@ -546,7 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ~120 cycles, several overlap).  Ring sizes are multiples of what keeps
     // a slot with one issuer, so each sees every phase of its slots.
     const int iss = warp - kWarpMma;
-    if (lane == 0 && iss < p.n_iss && u0 < u1) {
+    // The whole warp runs the loop and one elected lane issues: with uniform
+    // control flow the operands stay in uniform registers.
+    if (iss < p.n_iss && u0 < u1) {
       Seg s;
       seg_init(s, sched, p, u0, u1);
       // with two matrices issuer m has matrix m's tile of every k-block; with
@@ -565,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t x_step = p.x_slot_bytes >> 4;
       do {
         if (seg >= static_cast<uint32_t>(p.n_acc)) {
-          ok = mbar_wait(&bars->acc_empty[ab], (seg / p.n_acc - 1) & 1, &bars->abort, p.status);
+          ok = warp_wait(&bars->acc_empty[ab], (seg / p.n_acc - 1) & 1, bars, p.status);
           if (!ok) break;
           tc_fence_after();
         }
@@ -575,30 +588,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_kb = s.kb1 - s.kb0;
         int kb = skip;
         for (; kb < n_kb; kb += per) {
-          ok = mbar_wait(&bars->xfull[rx.slot], rx.use & 1, &bars->abort, p.status) &&
-               mbar_wait(&bars->afull[ra.slot], ra.use & 1, &bars->abort, p.status);
+          ok = warp_wait(&bars->xfull[rx.slot], rx.use & 1, bars, p.status) &&
+               warp_wait(&bars->afull[ra.slot], ra.use & 1, bars, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t a = tmem + p.a_col0 + static_cast<uint32_t>(ra.slot) * 32;
           const uint64_t b = x_desc0 + static_cast<uint64_t>(static_cast<uint32_t>(rx.slot) * x_step);
-          mma_ts(d, a, b, idesc, acc);
-          mma_ts(d, a + 8, b + 2, idesc, 1u);
-          mma_ts(d, a + 16, b + 4, idesc, 1u);
-          mma_ts(d, a + 24, b + 6, idesc, 1u);
+          if (elect_one()) {
+            mma_ts(d, a, b, idesc, acc);
+            mma_ts(d, a + 8, b + 2, idesc, 1u);
+            mma_ts(d, a + 16, b + 4, idesc, 1u);
+            mma_ts(d, a + 24, b + 6, idesc, 1u);
+            tc_commit(&bars->aempty[ra.slot]);
+            tc_commit(&bars->xempty[rx.slot]);
+          }
+          __syncwarp();
           acc = 1;
-          tc_commit(&bars->aempty[ra.slot]);
-          tc_commit(&bars->xempty[rx.slot]);
           ring_next(rx, p.sx, per);
           ring_next(ra, p.sa, kstep);
         }
         if (!ok) break;
         skip = kb - n_kb;
-        tc_commit(&bars->acc_full[ab]);
+        if (elect_one()) tc_commit(&bars->acc_full[ab]);
+        __syncwarp();
         ++seg;
         if (++ab == static_cast<uint32_t>(p.n_acc)) ab = 0;
       } while (seg_next(s, sched, p));
       // every MMA issued so far finishes before tensor memory is freed
-      tc_commit(&bars->drain[iss]);
+      if (elect_one()) tc_commit(&bars->drain[iss]);
+      __syncwarp();
       mbar_wait(&bars->drain[iss], 0, nullptr, p.status);
     }
     __syncwarp();

@@ -103,13 +103,20 @@ struct GParams {
   uint32_t* status;
 };
 
+// A tile shared by CTAs c_first..c_last whose last part this CTA delivered;
+// first_slot: the partial slot of c_first (the others use their slot 0).
+struct Todo {
+  int e, mt, slot0, nvalid, c_first, c_last, first_slot, pad;
+};
+
 struct GBars {
   uint64_t wfull[kMaxSlots], wempty[kMaxSlots];
   uint64_t xfull[kMaxSlots], xempty[kMaxSlots];
   uint64_t afull[kMaxSlots], aempty[kMaxSlots];
   uint64_t acc_full[2], acc_empty[2], drain[kMaxIssuers];
   uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
-  uint32_t tmem_base, abort, last_arriver, total;
+  uint32_t tmem_base, abort, total, n_todo;
+  Todo todo[2];
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -319,6 +326,95 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
   }
 }
 
+template <int NMAT, bool PAIR>
+__device__ __forceinline__ void load_bias(const GParams& p, int e, int mt, int r, float (&bias)[NMAT]) {
+#pragma unroll
+  for (int m = 0; m < NMAT; ++m) {
+    // (unclamped: the second half of an odd last pair is past p.N)
+    const int n = (PAIR ? 2 * mt + m : mt) * 128 + r;
+    bias[m] = p.bias && n < p.N
+                  ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.bias)[static_cast<int64_t>(e) * p.N + n])
+                  : 0.0f;
+  }
+}
+
+// Values of matrix row n for slots slot0 + 8 cc ..: activation, residual,
+// store.  Where rows of y start on 16 bytes the warp turns its 32 x 8 values
+// around in shared memory (`turn`, 1 KB of its own), so that a lane stores 8
+// consecutive ones.
+__device__ __forceinline__ void store8(const GParams& p, float (&v)[8], int cc, int n, int slot0, int nvalid,
+                                       float* turn) {
+  const int lane = threadIdx.x & 31;
+  const int cols = nvalid - cc * 8;
+  if (p.vec) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) turn[j * 32 + lane] = v[j];
+    __syncwarp();
+    const float4 q0 = *reinterpret_cast<const float4*>(turn + lane * 8);
+    const float4 q1 = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
+    __syncwarp();
+    const int n0 = n - lane + (lane & 3) * 8;  // lane l: slot l / 4, rows 8 (l % 4) ..
+    if ((lane >> 2) >= cols || n0 >= p.N) return;
+    float f[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    const int64_t i = static_cast<int64_t>(slot0 + cc * 8 + (lane >> 2)) * p.N + n0;
+    if (p.residual) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p.residual + i);
+      const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] += __uint_as_float(w4[j] << 16);
+        f[2 * j + 1] += __uint_as_float(w4[j] & 0xFFFF0000u);
+      }
+    }
+    if (p.out_fp32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.y) + i);
+      dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+      dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + i) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
+  if (n >= p.N) return;
+  int64_t i = static_cast<int64_t>(slot0 + cc * 8) * p.N + n;
+#pragma unroll 1
+  for (int j = 0; j < 8 && j < cols; ++j, i += p.N) {
+    float f = v[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) f = j == q ? v[q] : f;
+    if (p.residual) f += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
+    if (p.out_fp32) static_cast<float*>(p.y)[i] = f;
+    else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(f);
+  }
+}
+
+// Eight columns of a tile: the sums of its matrices (row r of the tile) to y.
+template <int NMAT, bool PAIR>
+__device__ __forceinline__ void emit(const GParams& p, float (&a)[NMAT][8], int cc, int mt, int slot0, int nvalid,
+                                     int r, const float (&bias)[NMAT], float* turn) {
+  if constexpr (NMAT == 2 && !PAIR) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[0][j] = silu_fast(a[0][j]) * a[1][j];
+    store8(p, a[0], cc, mt * 128 + r, slot0, nvalid, turn);
+  } else {
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[m][j] += bias[m];
+      }
+      activate(a[m], p.act);
+      store8(p, a[m], cc, (PAIR ? 2 * mt + m : mt) * 128 + r, slot0, nvalid, turn);
+    }
+  }
+}
+
 // Warp-wide load of 8 consecutive 32-bit columns of the thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -360,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kMaxIssuers; ++i) mbar_init(&bars->drain[i], 1);
     bars->abort = 0;
+    bars->n_todo = 0;
     mbar_fence_init();
   } else if (warp == kWarpX && lane == 0) {
     prefetch_tensormap(&tm_x);
@@ -719,7 +816,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w = warp & 3;  // TMEM lanes 32 w ..
       const int r = w * 32 + lane;
       const bool elected = warp == kWarpEpi && lane == 0;
-      volatile uint32_t* last_flag = &bars->last_arriver;
       Seg s;
       seg_init(s, sched, p, u0, u1);
       uint32_t seg = 0;
@@ -755,92 +851,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (p.n_iss == 2 && n_kb > 1) a[0][j] += __uint_as_float(v[1][j]);
           }
         };
-        // values of matrix row n, 8 slots: bias, activation, residual, store.
-        // Where rows of y start on 16 bytes the warp turns its 32 x 8 values
-        // around in shared memory, so that a lane stores 8 consecutive ones
-        auto store8 = [&](float (&v)[8], int cc, int n, float bias) {
-          if (NMAT == 1 || PAIR) {
-            if (p.bias) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += bias;
-            }
-            activate(v, p.act);
-          }
-          const int cols = s.nvalid - cc * 8;
-          if (p.vec) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) turn[j * 32 + lane] = v[j];
-            __syncwarp();
-            const float4 q0 = *reinterpret_cast<const float4*>(turn + lane * 8);
-            const float4 q1 = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
-            __syncwarp();
-            const int n0 = n - lane + (lane & 3) * 8;  // lane l: slot l / 4, rows 8 (l % 4) ..
-            if ((lane >> 2) >= cols || n0 >= p.N) return;
-            float f[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-            const int64_t i = static_cast<int64_t>(s.slot0 + cc * 8 + (lane >> 2)) * p.N + n0;
-            if ((NMAT == 1 || PAIR) && p.residual) {
-              const uint4 u = *reinterpret_cast<const uint4*>(p.residual + i);
-              const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                f[2 * j] += __uint_as_float(w4[j] << 16);
-                f[2 * j + 1] += __uint_as_float(w4[j] & 0xFFFF0000u);
-              }
-            }
-            if (p.out_fp32) {
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.y) + i);
-              dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-              dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-              uint32_t o[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-                o[j] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + i) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            return;
-          }
-          if (n >= p.N) return;
-          int64_t i = static_cast<int64_t>(s.slot0 + cc * 8) * p.N + n;
-#pragma unroll 1
-          for (int j = 0; j < 8 && j < cols; ++j, i += p.N) {
-            float f = v[0];
-#pragma unroll
-            for (int q = 1; q < 8; ++q) f = j == q ? v[q] : f;
-            if ((NMAT == 1 || PAIR) && p.residual)
-              f += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
-            if (p.out_fp32) static_cast<float*>(p.y)[i] = f;
-            else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(f);
-          }
-        };
-        int n[NMAT];
         float bias[NMAT];
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m) {
-          // (unclamped: the second half of an odd last pair is past p.N)
-          n[m] = (PAIR ? 2 * s.mt + m : s.mt) * 128 + r;
-          bias[m] = p.bias && n[m] < p.N ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
-                                               p.bias)[static_cast<int64_t>(s.e) * p.N + n[m]])
-                                         : 0.0f;
-        }
-        auto emit = [&](float (&a)[NMAT][8], int cc) {
-          if constexpr (NMAT == 2 && !PAIR) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) a[0][j] = silu_fast(a[0][j]) * a[1][j];
-            store8(a[0], cc, n[0], 0.0f);
-          } else {
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m) store8(a[m], cc, n[m], bias[m]);
-          }
-        };
+        load_bias<NMAT, PAIR>(p, s.e, s.mt, r, bias);
         if (n_kb == p.KB) {
 #pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
             float a[NMAT][8];
             own_sums(cc, a);
-            emit(a, cc);
+            emit<NMAT, PAIR>(p, a, cc, s.mt, s.slot0, s.nvalid, r, bias, turn);
           }
           tc_fence_before();
           __syncwarp();
@@ -876,39 +894,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // a CTA opens at most one tile that others finish: its counter
             const bool last = atom_add_acq_rel_gpu(p.counters + c_first, 1u) == static_cast<uint32_t>(n_contrib - 1);
             if (last) p.counters[c_first] = 0;  // all have arrived: ready for the next launch
-            *last_flag = last ? 1u : 0u;
-          }
-          group_sync();
-          if (*last_flag) {
-            const float* first = part(c_first);
-            const float* later = part(c_last) - 2 * p.partial_stride * c_last;  // slot 0 of the others
-#pragma unroll 1
-            for (int cc = 0; cc < n_chunks; ++cc) {
-              float a[NMAT][8];
-#pragma unroll
-              for (int m = 0; m < NMAT; ++m) {
-                const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 8;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[m][j] = 0.0f;
-#pragma unroll 4
-                for (int c = c_first; c <= c_last; ++c) {
-                  const float4* src =
-                      reinterpret_cast<const float4*>((c == c_first ? first : later + 2 * p.partial_stride * c) + at);
-                  const float4 v0 = __ldcg(src), v1 = __ldcg(src + 1);
-                  a[m][0] += v0.x;
-                  a[m][1] += v0.y;
-                  a[m][2] += v0.z;
-                  a[m][3] += v0.w;
-                  a[m][4] += v1.x;
-                  a[m][5] += v1.y;
-                  a[m][6] += v1.z;
-                  a[m][7] += v1.w;
-                }
-              }
-              emit(a, cc);
+            if (last) {
+              // every warp of the CTA adds the parts up once the roles are done
+              Todo& t = bars->todo[bars->n_todo++];
+              t.e = s.e;
+              t.mt = s.mt;
+              t.slot0 = s.slot0;
+              t.nvalid = s.nvalid;
+              t.c_first = c_first;
+              t.c_last = c_last;
+              t.first_slot = units_before(c_first, total, grid) >= s.tile_u ? 0 : 1;
             }
           }
-          group_sync();  // the flag word is used again by the next such tile
         }
         ++seg;
         first_tile += n_kb * NMAT;
@@ -921,6 +918,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  // ---- tiles shared by several CTAs that this one completes (at most its
+  // first and its last): the contributors' parts, added in CTA order.  The
+  // rings are idle now; their memory is where the warps turn values around.
+  for (int i = 0; i < static_cast<int>(bars->n_todo); ++i) {
+    const Todo t = bars->todo[i];
+    const int r = (warp & 3) * 32 + lane;
+    const int n_chunks = (t.nvalid + 7) >> 3;
+    float bias[NMAT];
+    load_bias<NMAT, PAIR>(p, t.e, t.mt, r, bias);
+    float* turn = reinterpret_cast<float*>(smem) + warp * 256;
+    const float* first = p.partials + (2 * static_cast<int64_t>(t.c_first) + t.first_slot) * p.partial_stride;
+#pragma unroll 1
+    for (int cc = warp >> 2; cc < n_chunks; cc += kThreads / 128) {
+      float a[NMAT][8];
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 8;
+        const float4* src = reinterpret_cast<const float4*>(first + at);
+        const float4 f0 = __ldcg(src), f1 = __ldcg(src + 1);
+        a[m][0] = f0.x;
+        a[m][1] = f0.y;
+        a[m][2] = f0.z;
+        a[m][3] = f0.w;
+        a[m][4] = f1.x;
+        a[m][5] = f1.y;
+        a[m][6] = f1.z;
+        a[m][7] = f1.w;
+#pragma unroll 4
+        for (int c = t.c_first + 1; c <= t.c_last; ++c) {
+          src = reinterpret_cast<const float4*>(p.partials + 2 * static_cast<int64_t>(c) * p.partial_stride + at);
+          const float4 v0 = __ldcg(src), v1 = __ldcg(src + 1);
+          a[m][0] += v0.x;
+          a[m][1] += v0.y;
+          a[m][2] += v0.z;
+          a[m][3] += v0.w;
+          a[m][4] += v1.x;
+          a[m][5] += v1.y;
+          a[m][6] += v1.z;
+          a[m][7] += v1.w;
+        }
+      }
+      emit<NMAT, PAIR>(p, a, cc, t.mt, t.slot0, t.nvalid, r, bias, turn);
+    }
   }
 }
 
@@ -1033,7 +1074,7 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   GPlan g;
   g.n_mt = static_cast<int>((N + 127) / 128);
   // large groups: two row tiles share each activation tile
-  g.pair = !swiglu && N > 128 && pick_cap(std::max(n_rows, 1), E, 1) > kPairCap;
+  g.pair = !swiglu && N > 128 && pick_cap(std::max(n_rows, 1), E, 1) > env_int("UW_GROUPED_PAIR", kPairCap);
   const int nmat = swiglu || g.pair ? 2 : 1;
   if (g.pair) g.n_mt = (g.n_mt + 1) / 2;
   if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;

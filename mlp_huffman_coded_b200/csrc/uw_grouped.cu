@@ -43,7 +43,6 @@
 //  * Barrier waits are bounded: a timeout records UW_ERR_TIMEOUT, drains
 //    copies and MMAs in flight, frees tensor memory and returns.
 #include <algorithm>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -994,10 +993,13 @@ __global__ void __launch_bounds__(256) permute_kernel(const PermuteParams p) {
 
 // ------------------------------- host side -----------------------------------
 
-// Rows per tile up to which scattered rows are gathered by TMA.
-constexpr int kGatherCap = 32;
-// Columns per tile above which two row tiles share the activation tile.
-constexpr int kPairCap = 64;
+// Rows per tile up to which scattered rows are gathered by TMA.  Measured with
+// SwiGLU products: 16 rows 62.4 us gathered, 63.6 laid next to each other
+// first; 32 rows 235.6 / 217.4.
+constexpr int kGatherCap = 16;
+// Two row tiles share the activation tile above this many columns per tile
+// and from this many units per CTA on (grouped_plan).
+constexpr int kPairCap = 64, kPairUnits = 128;
 
 struct GLayout {
   int cap = 16, n_iss = 1, n_acc = 1, sx = 2, sa = 2, sw = 2, vcap = 0;
@@ -1005,20 +1007,18 @@ struct GLayout {
   size_t smem = 0;
 };
 
-int env_int(const char* name, int dflt) {
-  const char* e = std::getenv(name);
-  return e ? std::atoi(e) : dflt;
-}
-
-// Columns per tile: what an average group needs, with room for uneven ones.
+// Columns per tile, at most: twice an average group's rows, since a group that
+// needs two column tiles has its weights rebuilt twice (they come from L2 the
+// second time), and at least 32, which costs little; one group takes what it
+// needs.  A wider tile than needed takes shared memory from the weight ring.
+// Measured with 8 experts of 14336 x 4096, SwiGLU: 8 rows on average 231 us at
+// 16 columns, 217 at 32; 64 rows 421 at 64, 267 at 128, 289 at 192.
 int pick_cap(int n_rows, int E, int nmat) {
-  const int most = nmat == 2 ? 192 : 256;
-  static int forced = env_int("UW_GROUPED_CAP", 0);
-  if (forced) return std::min(forced, most);
+  const int64_t most = nmat == 2 ? 192 : 256;
   int64_t want = n_rows;
-  if (E > 1) want = std::min<int64_t>(n_rows, 4 * ((static_cast<int64_t>(n_rows) + E - 1) / E));
+  if (E > 1) want = std::min<int64_t>(n_rows, std::max<int64_t>(32, 2 * ((static_cast<int64_t>(n_rows) + E - 1) / E)));
   const int64_t tiles = (want + most - 1) / most;
-  want = (want + tiles - 1) / tiles;
+  want = E > 1 ? std::min(want, most) : (want + tiles - 1) / tiles;
   return static_cast<int>(std::max<int64_t>(16, (want + 15) / 16 * 16));
 }
 
@@ -1041,7 +1041,9 @@ bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
   const uint32_t fixed = sched_bytes + turn_bytes + ((sizeof(GBars) + 127u) & ~127u) + 128u + 1024u;
   if (l.sa < step_a || fixed >= kSmemLimit / 2) return false;
   const uint32_t room = static_cast<uint32_t>(kSmemLimit) - fixed;
-  l.sx = l.cap <= 32 ? 8 : (l.cap <= 64 ? 6 : (l.cap <= 128 ? 4 : 3));
+  // measured: 8 slots at 16 columns (4: +2%), 4 at 192 (3: +2%, 5: +20%, the
+  // weight ring falls to 4 slots), 3 at 256 (4: +7%)
+  l.sx = l.cap <= 32 ? 8 : (l.cap <= 64 ? 6 : (l.cap <= 192 ? 4 : 3));
   l.sx -= l.sx % per;
   const uint32_t w_room = room - static_cast<uint32_t>(l.sx) * l.x_slot_bytes;
   l.sw = std::min(kMaxSlots, static_cast<int>(w_room / (kBody + kMinTail * 128u)));
@@ -1073,12 +1075,20 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
   GPlan g;
   g.n_mt = static_cast<int>((N + 127) / 128);
-  // large groups: two row tiles share each activation tile
-  g.pair = !swiglu && N > 128 && pick_cap(std::max(n_rows, 1), E, 1) > env_int("UW_GROUPED_PAIR", kPairCap);
+  g.KB = static_cast<int>(K / 64);
+  // Large groups: two row tiles share each activation tile, which halves what
+  // the activations cost in L2 and shared-memory traffic, where there are
+  // enough units that the coarser tiles do not cost more by being split.
+  // Measured, pairs against single tiles: 8 x 512 rows of 4096 x 14336 644 /
+  // 778 us, 8 x 64 rows 140 / 180; but 512 rows of one 14336 x 4096 matrix
+  // (73 pair units per CTA) 87 / 76.
+  const int cap1 = pick_cap(std::max(n_rows, 1), E, 1), cap2 = pick_cap(std::max(n_rows, 1), E, 2);
+  const int64_t pair_units =
+      static_cast<int64_t>((g.n_mt + 1) / 2) * std::max<int64_t>(E > 1 ? std::min(n_rows, E) : 1, n_rows / cap2) * g.KB;
+  g.pair = !swiglu && g.n_mt > 1 && cap1 > kPairCap && pair_units >= kPairUnits * sms;
   const int nmat = swiglu || g.pair ? 2 : 1;
   if (g.pair) g.n_mt = (g.n_mt + 1) / 2;
   if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
-  g.KB = static_cast<int>(K / 64);
   // the most units any split of n_rows into E groups can give
   const int64_t tiles = std::min<int64_t>(n_rows, n_rows / g.lay.cap + E);
   const int64_t units = tiles * g.n_mt * g.KB;
@@ -1218,9 +1228,10 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
                                CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
     return st;
   CUtensorMap tx64 = tx;
-  if (!gather && (st = make_tensor_map_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, static_cast<uint64_t>(a.K),
-                                          static_cast<uint64_t>(x_rows), static_cast<uint64_t>(a.K) * 2, 64, 64,
-                                          CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
+  if (!gather && g.lay.cap >= 64 &&
+      (st = make_tensor_map_2d(&tx64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, static_cast<uint64_t>(a.K),
+                               static_cast<uint64_t>(x_rows), static_cast<uint64_t>(a.K) * 2, 64, 64,
+                               CU_TENSOR_MAP_SWIZZLE_128B)) != UW_OK)
     return st;
   GParams p;
   std::memset(&p, 0, sizeof(p));

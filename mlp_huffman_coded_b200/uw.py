@@ -509,15 +509,22 @@ def mlp_stack(layers, pipelines, x, y, ws: Workspace, stream=None):
 # anything is launched.  BF16 tensors may be torch.bfloat16 or, as elsewhere
 # in this module, int16 views of it.
 
-_BF16, _FP32, _INT32 = ("torch.bfloat16", "torch.int16"), ("torch.float32",), ("torch.int32",)
+_DTYPES = {}  # element types a tensor argument may have, by name (torch is imported with the first call)
+
+
+def _dtypes(what):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update(bf16=(torch.bfloat16, torch.int16), fp32=(torch.float32,), int32=(torch.int32,))
+    return _DTYPES[what]
 
 
 def _tensor(t, what, types, shape, device):
-    """Checks a tensor argument; None stays None."""
+    """Address of a tensor argument after its checks; None stays None."""
     if t is None:
         return None
-    if str(t.dtype) not in types or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a contiguous {' or '.join(types)} {tuple(shape)} on {device} is "
+    if t.shape != shape or t.dtype not in _dtypes(types) or not t.is_contiguous() or t.device != device:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a contiguous {types} tensor of shape {tuple(shape)} on {device} is "
                                           f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -530,20 +537,22 @@ def _matrix_of(t, what):
 
 
 def _out_type(t, what):
-    if str(t.dtype) in _BF16:
-        return OUT_BF16
-    if str(t.dtype) in _FP32:
-        return OUT_FP32
+    """(uw_out_type, name) of a BF16 or FP32 tensor."""
+    if t.dtype in _dtypes("bf16"):
+        return OUT_BF16, "bf16"
+    if t.dtype in _dtypes("fp32"):
+        return OUT_FP32, "fp32"
     raise UwError(UW_ERR_INVALID_ARG, f"{what}: BF16 or FP32 is wanted, got {t.dtype}")
 
 
-def _call(fn, what, device, stream, *args):
+def _call(name, device, stream, *args):
     """One library call on `device`, whichever is current."""
     import torch
+    fn = getattr(_lib or lib(), name)
     if torch.cuda.current_device() != device.index:
         with torch.cuda.device(device):
-            return _check(fn(*args, _stream(stream)), what)
-    _check(fn(*args, _stream(stream)), what)
+            return _check(fn(*args, _stream(stream)), name)
+    _check(fn(*args, _stream(stream)), name)
 
 
 class Experts:
@@ -563,19 +572,11 @@ class Experts:
         self.table = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
         self.c = ExpertTable()
         arr = (C.POINTER(Matrix) * n)(*[C.pointer(m.mat) for m in self.matrices])
-        _call(lib().uw_experts_init, "uw_experts_init", self.device, stream, arr, n, self.table.data_ptr(), nbytes,
-              C.byref(self.c))
+        _call("uw_experts_init", self.device, stream, arr, n, self.table.data_ptr(), nbytes, C.byref(self.c))
+        self.rows, self.cols = int(self.c.rows), int(self.c.cols)
 
     def __len__(self):
-        return int(self.c.n_experts)
-
-    @property
-    def rows(self):
-        return int(self.c.rows)
-
-    @property
-    def cols(self):
-        return int(self.c.cols)
+        return len(self.matrices)
 
 
 def grouped_workspace_bytes(experts: Experts, n_rows: int, swiglu: bool = False) -> int:
@@ -587,13 +588,16 @@ def epilogue_workspace_bytes(dm_or_layout, batch: int) -> int:
     return int(lib().uw_gemm_epilogue_workspace_bytes(C.byref(L), batch))
 
 
-def _epilogue(device, n_groups, n_rows, rows, y, bias, activation, residual):
-    if activation not in ACTIVATIONS:
+def _epilogue(device, bias_shape, n_rows, rows, y, bias, activation, residual):
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise UwError(UW_ERR_INVALID_ARG, f"activation {activation!r}: one of {', '.join(ACTIVATIONS)}")
-    out = _out_type(y, "y")
-    e = Epilogue(_tensor(bias, "bias", _BF16, (rows,) if n_groups is None else (n_groups, rows), device),
-                 _tensor(residual, "residual", _BF16, (n_rows, rows), device), ACTIVATIONS[activation], out)
-    return e, _tensor(y, "y", _BF16 if out == OUT_BF16 else _FP32, (n_rows, rows), device)
+    out, types = _out_type(y, "y")
+    yp = _tensor(y, "y", types, (n_rows, rows), device)
+    if bias is None and residual is None and act == 0 and out == OUT_BF16:
+        return None, yp
+    return C.byref(Epilogue(_tensor(bias, "bias", "bf16", bias_shape, device),
+                            _tensor(residual, "residual", "bf16", (n_rows, rows), device), act, out)), yp
 
 
 def gemm_epilogue(dm: DeviceMatrix, x, y, ws: Workspace, bias=None, activation: str = "none", residual=None,
@@ -603,16 +607,17 @@ def gemm_epilogue(dm: DeviceMatrix, x, y, ws: Workspace, bias=None, activation: 
     [batch, rows]."""
     batch, _ = _matrix_of(x, "x")
     dev = dm.sm.device
-    e, yp = _epilogue(dev, None, batch, dm.rows, y, bias, activation, residual)
-    _call(lib().uw_gemm_epilogue, "uw_gemm_epilogue", dev, stream, C.byref(dm.mat),
-          _tensor(x, "x", _BF16, (batch, dm.cols), dev), batch, C.byref(e), yp, ws.ptr, ws.nbytes)
+    rows = dm.rows
+    e, yp = _epilogue(dev, (rows,), batch, rows, y, bias, activation, residual)
+    _call("uw_gemm_epilogue", dev, stream, C.byref(dm.mat),
+          _tensor(x, "x", "bf16", (batch, dm.cols), dev), batch, e, yp, ws.ptr, ws.nbytes)
 
 
 def _groups(experts, x, offsets, n_rows, rows):
     dev = experts.device
     x_rows, _ = _matrix_of(x, "x")
-    return (_tensor(x, "x", _BF16, (x_rows, experts.cols), dev), x_rows, _tensor(rows, "rows", _INT32, (n_rows,), dev),
-            _tensor(offsets, "offsets", _INT32, (len(experts) + 1,), dev), n_rows)
+    return (_tensor(x, "x", "bf16", (x_rows, experts.cols), dev), x_rows, _tensor(rows, "rows", "int32", (n_rows,), dev),
+            _tensor(offsets, "offsets", "int32", (len(experts) + 1,), dev), n_rows)
 
 
 def gemm_grouped(experts: Experts, x, offsets, y, ws: Workspace, rows=None, bias=None, activation: str = "none",
@@ -621,9 +626,9 @@ def gemm_grouped(experts: Experts, x, offsets, y, ws: Workspace, rows=None, bias
     [offsets[e], offsets[e+1]) of each expert e (uw_gemm_grouped): y BF16 or
     FP32 [n_rows, rows of W], bias BF16 [n_experts, rows of W]."""
     n_rows, _ = _matrix_of(y, "y")
-    e, yp = _epilogue(experts.device, len(experts), n_rows, experts.rows, y, bias, activation, residual)
-    _call(lib().uw_gemm_grouped, "uw_gemm_grouped", experts.device, stream, C.byref(experts.c),
-          *_groups(experts, x, offsets, n_rows, rows), C.byref(e), yp, ws.ptr, ws.nbytes)
+    e, yp = _epilogue(experts.device, (len(experts), experts.rows), n_rows, experts.rows, y, bias, activation, residual)
+    _call("uw_gemm_grouped", experts.device, stream, C.byref(experts.c),
+          *_groups(experts, x, offsets, n_rows, rows), e, yp, ws.ptr, ws.nbytes)
 
 
 def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace, rows=None, stream=None):
@@ -632,8 +637,8 @@ def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace
     n_rows, _ = _matrix_of(h, "h")
     if up.device != gate.device:
         raise UwError(UW_ERR_INVALID_ARG, "gate and up on different devices")
-    _call(lib().uw_gemm_grouped_swiglu, "uw_gemm_grouped_swiglu", gate.device, stream, C.byref(gate.c), C.byref(up.c),
-          *_groups(gate, x, offsets, n_rows, rows), _tensor(h, "h", _BF16, (n_rows, gate.rows), gate.device), ws.ptr,
+    _call("uw_gemm_grouped_swiglu", gate.device, stream, C.byref(gate.c), C.byref(up.c),
+          *_groups(gate, x, offsets, n_rows, rows), _tensor(h, "h", "bf16", (n_rows, gate.rows), gate.device), ws.ptr,
           ws.nbytes)
 
 
@@ -658,9 +663,9 @@ def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:
 def moe_route(logits, route: Route, ws: Workspace, renormalize: bool = True, stream=None):
     """Top-k routing of logits [n_tokens, n_experts] (BF16 or FP32) into
     `route` (uw_moe_route)."""
-    typ = _out_type(logits, "logits")
-    lp = _tensor(logits, "logits", _BF16 if typ == OUT_BF16 else _FP32, (route.n_tokens, route.n_experts), route.device)
-    _call(lib().uw_moe_route, "uw_moe_route", route.device, stream, lp, typ, route.n_tokens, route.n_experts,
+    typ, types = _out_type(logits, "logits")
+    lp = _tensor(logits, "logits", types, (route.n_tokens, route.n_experts), route.device)
+    _call("uw_moe_route", route.device, stream, lp, typ, route.n_tokens, route.n_experts,
           route.top_k, int(renormalize), route.weights.data_ptr(), route.experts.data_ptr(), route.slots.data_ptr(),
           route.rows.data_ptr(), route.offsets.data_ptr(), ws.ptr, ws.nbytes)
 
@@ -670,12 +675,13 @@ def moe_combine(parts, slots, weights, y, residual=None, stream=None):
     (uw_moe_combine): parts FP32 or BF16 [n_rows, cols]."""
     n_rows, cols = _matrix_of(parts, "parts")
     n_tokens, top_k = _matrix_of(slots, "slots")
-    dev, typ = parts.device, _out_type(parts, "parts")
-    _call(lib().uw_moe_combine, "uw_moe_combine", dev, stream,
-          _tensor(parts, "parts", _BF16 if typ == OUT_BF16 else _FP32, (n_rows, cols), dev), typ,
-          _tensor(slots, "slots", _INT32, (n_tokens, top_k), dev),
-          _tensor(weights, "weights", _FP32, (n_tokens, top_k), dev), n_tokens, top_k, cols, n_rows,
-          _tensor(residual, "residual", _BF16, (n_tokens, cols), dev), _tensor(y, "y", _BF16, (n_tokens, cols), dev))
+    dev = parts.device
+    typ, types = _out_type(parts, "parts")
+    _call("uw_moe_combine", dev, stream,
+          _tensor(parts, "parts", types, (n_rows, cols), dev), typ,
+          _tensor(slots, "slots", "int32", (n_tokens, top_k), dev),
+          _tensor(weights, "weights", "fp32", (n_tokens, top_k), dev), n_tokens, top_k, cols, n_rows,
+          _tensor(residual, "residual", "bf16", (n_tokens, cols), dev), _tensor(y, "y", "bf16", (n_tokens, cols), dev))
 
 
 def moe_workspace_bytes(gate: Experts, up: Experts, down: Experts, n_tokens: int, top_k: int) -> int:
@@ -687,14 +693,15 @@ def moe_block(gate: Experts, up: Experts, down: Experts, x, logits, top_k: int, 
     """Sparse SwiGLU MLP block (uw_moe_block): y[t] = residual[t] + sum over
     token t's top_k experts of weight * W_down (SiLU(W_gate x) * (W_up x))."""
     n_tokens, _ = _matrix_of(x, "x")
-    dev, typ = gate.device, _out_type(logits, "logits")
+    dev = gate.device
+    typ, types = _out_type(logits, "logits")
     if up.device != dev or down.device != dev:
         raise UwError(UW_ERR_INVALID_ARG, "gate, up and down on different devices")
     shape = (n_tokens, gate.cols)
-    _call(lib().uw_moe_block, "uw_moe_block", dev, stream, C.byref(gate.c), C.byref(up.c), C.byref(down.c),
-          _tensor(logits, "logits", _BF16 if typ == OUT_BF16 else _FP32, (n_tokens, len(gate)), dev), typ, top_k,
-          int(renormalize), _tensor(x, "x", _BF16, shape, dev), n_tokens,
-          _tensor(residual, "residual", _BF16, shape, dev), _tensor(y, "y", _BF16, shape, dev), ws.ptr, ws.nbytes)
+    _call("uw_moe_block", dev, stream, C.byref(gate.c), C.byref(up.c), C.byref(down.c),
+          _tensor(logits, "logits", types, (n_tokens, len(gate)), dev), typ, top_k,
+          int(renormalize), _tensor(x, "x", "bf16", shape, dev), n_tokens,
+          _tensor(residual, "residual", "bf16", shape, dev), _tensor(y, "y", "bf16", shape, dev), ws.ptr, ws.nbytes)
 
 
 def autotune(dm: DeviceMatrix, batches, reps: int, x, y, ws: Workspace, flush=None, stream=None):

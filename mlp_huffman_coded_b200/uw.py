@@ -509,23 +509,27 @@ def mlp_stack(layers, pipelines, x, y, ws: Workspace, stream=None):
 # anything is launched.  BF16 tensors may be torch.bfloat16 or, as elsewhere
 # in this module, int16 views of it.
 
-_DTYPES = {}  # element types a tensor argument may have, by name (torch is imported with the first call)
+_torch = None  # torch, imported with the first of these calls
+_BF16 = _FP32 = _INT32 = ()  # the element types a tensor argument may have
 
 
-def _dtypes(what):
-    if not _DTYPES:
+def _need_torch():
+    global _torch, _BF16, _FP32, _INT32
+    if _torch is None:
         import torch
-        _DTYPES.update(bf16=(torch.bfloat16, torch.int16), fp32=(torch.float32,), int32=(torch.int32,))
-    return _DTYPES[what]
+        _BF16, _FP32, _INT32 = (torch.bfloat16, torch.int16), (torch.float32,), (torch.int32,)
+        _torch = torch
 
 
 def _tensor(t, what, types, shape, device):
-    """Address of a tensor argument after its checks; None stays None."""
+    """Address of a tensor argument after its checks (`device`: CUDA ordinal);
+    None stays None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype not in _dtypes(types) or not t.is_contiguous() or t.device != device:
-        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a contiguous {types} tensor of shape {tuple(shape)} on {device} is "
-                                          f"wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.dtype not in types or t.get_device() != device or not t.is_contiguous():
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a contiguous {' or '.join(map(str, types))} tensor of shape "
+                                          f"{tuple(shape)} on cuda:{device} is wanted, got {t.dtype} {tuple(t.shape)} "
+                                          f"on {t.device}")
     return t.data_ptr()
 
 
@@ -537,39 +541,53 @@ def _matrix_of(t, what):
 
 
 def _out_type(t, what):
-    """(uw_out_type, name) of a BF16 or FP32 tensor."""
-    if t.dtype in _dtypes("bf16"):
-        return OUT_BF16, "bf16"
-    if t.dtype in _dtypes("fp32"):
-        return OUT_FP32, "fp32"
+    """(uw_out_type, element types) of a BF16 or FP32 tensor."""
+    if _torch is None:
+        _need_torch()
+    if t.dtype in _BF16:
+        return OUT_BF16, _BF16
+    if t.dtype in _FP32:
+        return OUT_FP32, _FP32
     raise UwError(UW_ERR_INVALID_ARG, f"{what}: BF16 or FP32 is wanted, got {t.dtype}")
 
 
+def _space(ws, device):
+    """Address and size of a workspace on `device`."""
+    if ws.t.get_device() != device:
+        raise UwError(UW_ERR_INVALID_ARG, f"workspace: one on cuda:{device} is wanted, got {ws.t.device}")
+    return ws.ptr, ws.nbytes
+
+
 def _call(name, device, stream, *args):
-    """One library call on `device`, whichever is current."""
-    import torch
+    """One library call on `device` (a CUDA ordinal), whichever is current.
+    The current stream is asked for by its raw handle: building the Stream
+    object of _stream() takes 3 us, as long as the launch."""
+    if device < 0:
+        raise UwError(UW_ERR_INVALID_ARG, f"{name}: tensors on a CUDA device are wanted")
     fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _check(fn(*args, _stream(stream)), name)
-    _check(fn(*args, _stream(stream)), name)
+    st = _torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if _torch.cuda.current_device() != device:
+        with _torch.cuda.device(device):
+            return _check(fn(*args, st), name)
+    _check(fn(*args, st), name)
 
 
 class Experts:
     """One compressed matrix per expert (same shape, direct-palette form), as
-    the grouped products take them (uw_experts_init).  Keeps the matrices."""
+    the grouped products take them (uw_experts_init).  Keeps the matrices;
+    their direct-palette form must not be prepared again afterwards."""
 
     def __init__(self, matrices, stream=None):
-        import torch
+        _need_torch()
         self.matrices = list(matrices)
         if not self.matrices:
             raise UwError(UW_ERR_INVALID_ARG, "Experts: no matrices")
-        self.device = self.matrices[0].sm.device
-        if any(m.sm.device != self.device for m in self.matrices):
+        self.device = self.matrices[0].sm.get_device()
+        if any(m.sm.get_device() != self.device for m in self.matrices):
             raise UwError(UW_ERR_INVALID_ARG, "Experts: matrices on different devices")
         n = len(self.matrices)
         nbytes = int(lib().uw_experts_table_bytes(n))
-        self.table = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+        self.table = _torch.empty(max(nbytes, 16), dtype=_torch.uint8, device=f"cuda:{self.device}")
         self.c = ExpertTable()
         arr = (C.POINTER(Matrix) * n)(*[C.pointer(m.mat) for m in self.matrices])
         _call("uw_experts_init", self.device, stream, arr, n, self.table.data_ptr(), nbytes, C.byref(self.c))
@@ -596,8 +614,8 @@ def _epilogue(device, bias_shape, n_rows, rows, y, bias, activation, residual):
     yp = _tensor(y, "y", types, (n_rows, rows), device)
     if bias is None and residual is None and act == 0 and out == OUT_BF16:
         return None, yp
-    return C.byref(Epilogue(_tensor(bias, "bias", "bf16", bias_shape, device),
-                            _tensor(residual, "residual", "bf16", (n_rows, rows), device), act, out)), yp
+    return C.byref(Epilogue(_tensor(bias, "bias", _BF16, bias_shape, device),
+                            _tensor(residual, "residual", _BF16, (n_rows, rows), device), act, out)), yp
 
 
 def gemm_epilogue(dm: DeviceMatrix, x, y, ws: Workspace, bias=None, activation: str = "none", residual=None,
@@ -606,18 +624,18 @@ def gemm_epilogue(dm: DeviceMatrix, x, y, ws: Workspace, bias=None, activation: 
     cols], y BF16 or FP32 [batch, rows], bias BF16 [rows], residual BF16
     [batch, rows]."""
     batch, _ = _matrix_of(x, "x")
-    dev = dm.sm.device
+    dev = dm.sm.get_device()
     rows = dm.rows
     e, yp = _epilogue(dev, (rows,), batch, rows, y, bias, activation, residual)
     _call("uw_gemm_epilogue", dev, stream, C.byref(dm.mat),
-          _tensor(x, "x", "bf16", (batch, dm.cols), dev), batch, e, yp, ws.ptr, ws.nbytes)
+          _tensor(x, "x", _BF16, (batch, dm.cols), dev), batch, e, yp, *_space(ws, dev))
 
 
 def _groups(experts, x, offsets, n_rows, rows):
     dev = experts.device
     x_rows, _ = _matrix_of(x, "x")
-    return (_tensor(x, "x", "bf16", (x_rows, experts.cols), dev), x_rows, _tensor(rows, "rows", "int32", (n_rows,), dev),
-            _tensor(offsets, "offsets", "int32", (len(experts) + 1,), dev), n_rows)
+    return (_tensor(x, "x", _BF16, (x_rows, experts.cols), dev), x_rows, _tensor(rows, "rows", _INT32, (n_rows,), dev),
+            _tensor(offsets, "offsets", _INT32, (len(experts) + 1,), dev), n_rows)
 
 
 def gemm_grouped(experts: Experts, x, offsets, y, ws: Workspace, rows=None, bias=None, activation: str = "none",
@@ -628,7 +646,8 @@ def gemm_grouped(experts: Experts, x, offsets, y, ws: Workspace, rows=None, bias
     n_rows, _ = _matrix_of(y, "y")
     e, yp = _epilogue(experts.device, (len(experts), experts.rows), n_rows, experts.rows, y, bias, activation, residual)
     _call("uw_gemm_grouped", experts.device, stream, C.byref(experts.c),
-          *_groups(experts, x, offsets, n_rows, rows), e, yp, ws.ptr, ws.nbytes)
+          *_groups(experts, x, offsets, n_rows, rows), e, yp,
+          *_space(ws, experts.device))
 
 
 def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace, rows=None, stream=None):
@@ -638,8 +657,8 @@ def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace
     if up.device != gate.device:
         raise UwError(UW_ERR_INVALID_ARG, "gate and up on different devices")
     _call("uw_gemm_grouped_swiglu", gate.device, stream, C.byref(gate.c), C.byref(up.c),
-          *_groups(gate, x, offsets, n_rows, rows), _tensor(h, "h", "bf16", (n_rows, gate.rows), gate.device), ws.ptr,
-          ws.nbytes)
+          *_groups(gate, x, offsets, n_rows, rows), _tensor(h, "h", _BF16, (n_rows, gate.rows), gate.device),
+          *_space(ws, gate.device))
 
 
 class Route:
@@ -653,7 +672,7 @@ class Route:
         self.slots = torch.empty(n_tokens, top_k, dtype=torch.int32, device=device)
         self.rows = torch.empty(n_tokens * top_k, dtype=torch.int32, device=device)
         self.offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=device)
-        self.device = self.weights.device
+        self.device = self.weights.get_device()
 
 
 def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:
@@ -667,7 +686,7 @@ def moe_route(logits, route: Route, ws: Workspace, renormalize: bool = True, str
     lp = _tensor(logits, "logits", types, (route.n_tokens, route.n_experts), route.device)
     _call("uw_moe_route", route.device, stream, lp, typ, route.n_tokens, route.n_experts,
           route.top_k, int(renormalize), route.weights.data_ptr(), route.experts.data_ptr(), route.slots.data_ptr(),
-          route.rows.data_ptr(), route.offsets.data_ptr(), ws.ptr, ws.nbytes)
+          route.rows.data_ptr(), route.offsets.data_ptr(), *_space(ws, route.device))
 
 
 def moe_combine(parts, slots, weights, y, residual=None, stream=None):
@@ -675,13 +694,13 @@ def moe_combine(parts, slots, weights, y, residual=None, stream=None):
     (uw_moe_combine): parts FP32 or BF16 [n_rows, cols]."""
     n_rows, cols = _matrix_of(parts, "parts")
     n_tokens, top_k = _matrix_of(slots, "slots")
-    dev = parts.device
+    dev = parts.get_device()
     typ, types = _out_type(parts, "parts")
     _call("uw_moe_combine", dev, stream,
           _tensor(parts, "parts", types, (n_rows, cols), dev), typ,
-          _tensor(slots, "slots", "int32", (n_tokens, top_k), dev),
-          _tensor(weights, "weights", "fp32", (n_tokens, top_k), dev), n_tokens, top_k, cols, n_rows,
-          _tensor(residual, "residual", "bf16", (n_tokens, cols), dev), _tensor(y, "y", "bf16", (n_tokens, cols), dev))
+          _tensor(slots, "slots", _INT32, (n_tokens, top_k), dev),
+          _tensor(weights, "weights", _FP32, (n_tokens, top_k), dev), n_tokens, top_k, cols, n_rows,
+          _tensor(residual, "residual", _BF16, (n_tokens, cols), dev), _tensor(y, "y", _BF16, (n_tokens, cols), dev))
 
 
 def moe_workspace_bytes(gate: Experts, up: Experts, down: Experts, n_tokens: int, top_k: int) -> int:
@@ -700,8 +719,9 @@ def moe_block(gate: Experts, up: Experts, down: Experts, x, logits, top_k: int, 
     shape = (n_tokens, gate.cols)
     _call("uw_moe_block", dev, stream, C.byref(gate.c), C.byref(up.c), C.byref(down.c),
           _tensor(logits, "logits", types, (n_tokens, len(gate)), dev), typ, top_k,
-          int(renormalize), _tensor(x, "x", "bf16", shape, dev), n_tokens,
-          _tensor(residual, "residual", "bf16", shape, dev), _tensor(y, "y", "bf16", shape, dev), ws.ptr, ws.nbytes)
+          int(renormalize), _tensor(x, "x", _BF16, shape, dev), n_tokens,
+          _tensor(residual, "residual", _BF16, shape, dev), _tensor(y, "y", _BF16, shape, dev),
+          *_space(ws, dev))
 
 
 def autotune(dm: DeviceMatrix, batches, reps: int, x, y, ws: Workspace, flush=None, stream=None):

@@ -169,6 +169,33 @@ def test_block_refusals():
     assert block(T=0) == uw.UW_OK
 
 
+def test_the_binding_checks_its_tensors():
+    import torch
+    uw._need_torch()
+    good = torch.zeros(4, 8, dtype=torch.bfloat16)
+    dev = good.get_device()  # -1: these live on the CPU
+    assert uw._tensor(good, "t", uw._BF16, (4, 8), dev) == good.data_ptr()
+    assert uw._tensor(good.view(torch.int16), "t", uw._BF16, (4, 8), dev) == good.data_ptr()
+    assert uw._tensor(None, "t", uw._BF16, (4, 8), dev) is None
+    for bad, types, shape, d in ((good, uw._BF16, (4, 9), dev), (good, uw._BF16, (32,), dev), (good, uw._FP32, (4, 8), dev),
+                                 (good.t(), uw._BF16, (8, 4), dev), (good[:, ::2], uw._BF16, (4, 4), dev),
+                                 (good, uw._BF16, (4, 8), 0)):
+        with pytest.raises(uw.UwError) as e:
+            uw._tensor(bad, "t", types, shape, d)
+        assert e.value.status == uw.UW_ERR_INVALID_ARG
+    for t in (None, torch.zeros(3), torch.zeros(2, 2, 2)):
+        with pytest.raises(uw.UwError):
+            uw._matrix_of(t, "t")
+    with pytest.raises(uw.UwError):
+        uw._out_type(torch.zeros(2, dtype=torch.float16), "t")
+    with pytest.raises(uw.UwError):
+        uw._epilogue(dev, (8,), 4, 8, good, None, "swish", None)
+    # tensors that are on no CUDA device at all
+    with pytest.raises(uw.UwError) as e:
+        uw.moe_combine(torch.zeros(4, 8), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2), good[:2].contiguous())
+    assert e.value.status == uw.UW_ERR_INVALID_ARG
+
+
 def test_the_plain_forms_themselves():
     """The references of the GPU tests at values worked by hand."""
     assert act_f64([-1.0, 2.0], "relu").tolist() == [0.0, 2.0]

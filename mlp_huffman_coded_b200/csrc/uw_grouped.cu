@@ -19,11 +19,12 @@
 //  * W is the MMA's A operand (128 weight rows = 128 TMEM lanes), the rows of
 //    the group are the N side (16..256 columns): decode-time groups of a few
 //    rows cost one N = 16 MMA, and nothing is padded to 128 rows.
-//  * The unit of work is one 64-column k-block of one (group, 128-row tile,
-//    column tile).  Group sizes are read on the device; every CTA computes
-//    the same table of units and takes an equal contiguous share (stream-K),
-//    so ragged groups, few large tiles and many small ones balance alike.
-//    A group without rows has no units: its weights are never read.
+//  * The work is tiles (group, 128 weight rows, columns) of K / 64 k-blocks.
+//    Group sizes are read on the device; every CTA computes the same table of
+//    tiles and takes whole tiles in waves and then an equal run of the k-blocks
+//    that are left (stream-K), so ragged groups, few large tiles and many
+//    small ones balance alike.  A group without rows has no tiles: its weights
+//    are never read.
 //  * Every ring slot carries ONE tile record (12304 bytes and its verbatim
 //    rows): it goes back to the producer as soon as that tile is rebuilt, so
 //    nearly all of the weight ring is in flight to HBM at any time.
@@ -71,7 +72,7 @@ constexpr size_t kSmemFloor = 120 * 1024;  // one CTA (and one owner of tensor m
 
 // One group's share of the schedule.
 struct SchedEntry {
-  int unit0;      // first unit
+  int tile0;      // first tile
   int start;      // first slot
   int count;      // slots
   int n_nt;       // column tiles in bits 16.., columns per tile (multiple of 16) in bits 0..15
@@ -114,7 +115,7 @@ struct GBars {
   uint64_t afull[kMaxSlots], aempty[kMaxSlots];
   uint64_t acc_full[2], acc_empty[2], drain[kMaxIssuers];
   uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
-  uint32_t tmem_base, abort, total, n_todo;
+  uint32_t tmem_base, abort, tiles, n_todo;
   Todo todo[2];
 };
 
@@ -166,56 +167,102 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
 }
 
 // ------------------------------- schedule ------------------------------------
-// A CTA's units [u0, u1) as segments: runs of k-blocks of one (group, row
-// tile, column tile).  Every role walks the same sequence.
+// The tiles (group, row tile, column tile), column tiles of a row tile next to
+// each other, are dealt out in waves of one tile per CTA: CTAs that work at
+// the same time share weight tiles (the column tiles of a row tile) and
+// activation tiles through L2.  What does not fill waves evenly, between one
+// and two tiles per CTA (or everything, when there are fewer tiles), is cut
+// into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
+// instead read the weights of three column tiles three times from HBM: the
+// first CTA's second column tile came when L2 had long moved on.
+struct Share {
+  int grid, waves;  // CTAs that take part, whole tiles per CTA
+  int sk_units;     // k-blocks of the tiles after the waves
+  int u0, u1;       // this CTA's run of them
+};
+// A CTA's work as segments: runs of k-blocks of one tile.  Every role walks
+// the same sequence.
 struct Seg {
-  int u, u1;          // next unit, end of the CTA's share
-  int e, mt, nt;      // of the segment
+  int wave, u;        // waves done, next k-block of the run
+  int e, mt, nt;
   int kb0, kb1;
   int ntile, slot0, nvalid;
-  int tile_u;         // first unit of the whole tile
+  int tile_u;         // first k-block of the whole tile in the run's count
 };
 
 __device__ __forceinline__ int units_before(int c, int total, int grid) {
   return static_cast<int>(static_cast<long long>(c) * total / grid);
 }
-// CTA whose share holds unit u
+// CTA whose run holds unit u
 __device__ __forceinline__ int unit_owner(int u, int total, int grid) {
   return static_cast<int>((static_cast<long long>(u + 1) * grid - 1) / total);
 }
 
-__device__ __forceinline__ void seg_fill(Seg& s, const SchedEntry* sched, const GParams& p, int local) {
+__device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) {
+  Share h;
+  // with fewer k-blocks than CTAs the last CTAs have none: every CTA that the
+  // shares count has at least one
+  h.grid = min(p.grid, tiles * p.KB);
+  h.waves = h.sk_units = h.u0 = h.u1 = 0;
+  if (cta >= h.grid) return h;
+  const int full = tiles / h.grid, rest = tiles - full * h.grid;
+  h.waves = rest && full ? full - 1 : full;
+  h.sk_units = (tiles - h.waves * h.grid) * p.KB;
+  if (h.sk_units) {
+    h.u0 = units_before(cta, h.sk_units, h.grid);
+    h.u1 = units_before(cta + 1, h.sk_units, h.grid);
+  }
+  return h;
+}
+
+__device__ __forceinline__ void seg_fill(Seg& s, const SchedEntry* sched, const GParams& p, int tile) {
+  // the last entry with tile0 <= tile, from the current one on (entries
+  // without tiles share their successor's tile0)
+  if (tile >= sched[s.e + 1].tile0) {
+    int lo = s.e + 1, hi = p.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sched[mid].tile0 <= tile) lo = mid;
+      else hi = mid;
+    }
+    s.e = lo;
+  }
   const SchedEntry en = sched[s.e];
   const int n_nt = en.n_nt >> 16;
-  const int tile = local / p.KB;
-  s.kb0 = local - tile * p.KB;
-  s.mt = tile / n_nt;
-  s.nt = tile - s.mt * n_nt;
+  const int local = tile - en.tile0;
+  s.mt = local / n_nt;
+  s.nt = local - s.mt * n_nt;
   s.ntile = en.n_nt & 0xFFFF;
   s.slot0 = en.start + s.nt * s.ntile;
   s.nvalid = min(s.ntile, en.count - s.nt * s.ntile);
-  s.tile_u = s.u - s.kb0;
-  s.kb1 = min(p.KB, s.kb0 + (s.u1 - s.u));
 }
-// first segment at unit s.u (s.u < s.u1)
-__device__ __forceinline__ void seg_init(Seg& s, const SchedEntry* sched, const GParams& p, int u0, int u1) {
-  s.u = u0;
-  s.u1 = u1;
-  int lo = 0, hi = p.E;  // last entry with unit0 <= u0 (entries without units share their successor's unit0)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sched[mid].unit0 <= u0) lo = mid;
-    else hi = mid;
+__device__ __forceinline__ void seg_here(Seg& s, const SchedEntry* sched, const GParams& p, const Share& h, int cta) {
+  if (s.wave < h.waves) {
+    s.kb0 = 0;
+    s.kb1 = p.KB;
+    seg_fill(s, sched, p, s.wave * h.grid + cta);
+  } else {
+    const int tile = s.u / p.KB;
+    s.kb0 = s.u - tile * p.KB;
+    s.kb1 = min(p.KB, s.kb0 + (h.u1 - s.u));
+    s.tile_u = s.u - s.kb0;
+    seg_fill(s, sched, p, h.waves * h.grid + tile);
   }
-  s.e = lo;
-  seg_fill(s, sched, p, u0 - sched[lo].unit0);
+}
+// first segment of a share that is not empty
+__device__ __forceinline__ void seg_init(Seg& s, const SchedEntry* sched, const GParams& p, const Share& h, int cta) {
+  s.wave = 0;
+  s.u = h.u0;
+  s.e = 0;
+  s.tile_u = 0;
+  seg_here(s, sched, p, h, cta);
 }
 // false when the share is done
-__device__ __forceinline__ bool seg_next(Seg& s, const SchedEntry* sched, const GParams& p) {
-  s.u += s.kb1 - s.kb0;
-  if (s.u >= s.u1) return false;
-  while (s.u >= sched[s.e + 1].unit0) ++s.e;
-  seg_fill(s, sched, p, s.u - sched[s.e].unit0);
+__device__ __forceinline__ bool seg_next(Seg& s, const SchedEntry* sched, const GParams& p, const Share& h, int cta) {
+  if (s.wave < h.waves) ++s.wave;
+  else s.u += s.kb1 - s.kb0;
+  if (s.wave >= h.waves && s.u >= h.u1) return false;
+  seg_here(s, sched, p, h, cta);
   return true;
 }
 
@@ -435,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
 
-  // ---- set-up: barriers, tensor memory and the table of units
+  // ---- set-up: barriers, tensor memory and the table of tiles
   if (warp == kWarpW && lane == 0) {
     for (int s = 0; s < p.sw; ++s) {
       mbar_init(&bars->wfull[s], 1);
@@ -479,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = bad ? 0 : b - a;
       const int n_nt = (cnt + p.cap - 1) / p.cap;
       const int ntile = n_nt ? ((cnt + n_nt - 1) / n_nt + 15) / 16 * 16 : 16;
-      const int units = n_nt * p.n_mt * p.KB;
-      int incl = units;
+      const int tiles = n_nt * p.n_mt;
+      int incl = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -488,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (e < p.E) {
         SchedEntry en;
-        en.unit0 = base + incl - units;
+        en.tile0 = base + incl - tiles;
         en.start = a;
         en.count = cnt;
         en.n_nt = (n_nt << 16) | ntile;
@@ -499,21 +546,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bad = __any_sync(0xFFFFFFFFu, bad);
     if (lane == 0) {
       if (bad) record_status(p.status, UW_ERR_INVALID_ARG);
-      sched[p.E].unit0 = bad ? 0 : base;
-      bars->total = bad ? 0 : base;
+      sched[p.E].tile0 = bad ? 0 : base;
+      bars->tiles = bad ? 0 : base;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int total = static_cast<int>(bars->total);
-  // with fewer units than CTAs the last CTAs have none: every CTA that the
-  // shares count has at least one
-  const int grid = min(p.grid, total);
   const int cta = static_cast<int>(blockIdx.x);
-  const int u0 = cta < grid ? units_before(cta, total, grid) : 0;
-  const int u1 = cta < grid ? units_before(cta + 1, total, grid) : 0;
+  const Share share = share_of(cta, static_cast<int>(bars->tiles), p);
+  const bool work = share.waves > 0 || share.u0 < share.u1;
   auto desc = [&](int m, int e) -> const ExpertDesc* { return p.table[m] ? p.table[m] + e : &p.one; };
 
   if (warp == kWarpW) {
@@ -523,10 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // thread alone took about 650 cycles per tile, more than HBM needs for
     // one (530).  The lanes hold the verbatim offsets of the next 31 k-blocks.
     constexpr int kSpan = 28;  // k-blocks per set of offsets: whole batches, and one offset more
-    if (u0 < u1) {
+    if (work) {
       const uint64_t once = l2_evict_first();
       Seg s;
-      seg_init(s, sched, p, u0, u1);
+      seg_init(s, sched, p, share, cta);
       Ring rw{0, 0};
       int issued = 0;
       bool ok = true;
@@ -590,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           v0 = w0;
           v1 = w1;
         }
-      } while (ok && seg_next(s, sched, p));
+      } while (ok && seg_next(s, sched, p, share, cta));
       // every issued copy lands before the CTA exits (already so unless a
       // wait gave up)
       if (lane == 0)
@@ -600,10 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpX) {
     // ------------------------- activation producer --------------------------
-    if (u0 < u1) {
+    if (work) {
       griddep_wait();
       Seg s;
-      seg_init(s, sched, p, u0, u1);
+      seg_init(s, sched, p, share, cta);
       Ring rx{0, 0};
       int issued = 0;
       bool ok = true;
@@ -640,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
           ring_next(rx, p.sx);
         }
-      } while (ok && seg_next(s, sched, p));
+      } while (ok && seg_next(s, sched, p, share, cta));
       if (lane == 0)
         for (int q = max(0, issued - p.sx); q < issued; ++q)
           mbar_wait(&bars->xfull[q % p.sx], static_cast<uint32_t>(q / p.sx) & 1, nullptr, p.status);
@@ -655,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int iss = warp - kWarpMma;
     // The whole warp runs the loop and one elected lane issues: with uniform
     // control flow the operands stay in uniform registers.
-    if (iss < p.n_iss && u0 < u1) {
+    if (iss < p.n_iss && work) {
       Seg s;
-      seg_init(s, sched, p, u0, u1);
+      seg_init(s, sched, p, share, cta);
       // with two matrices issuer m has matrix m's tile of every k-block; with
       // one, the issuers take turns
       const int per = p.n_iss / NMAT, kstep = NMAT * per;
@@ -709,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++seg;
         if (++ab == static_cast<uint32_t>(p.n_acc)) ab = 0;
-      } while (seg_next(s, sched, p));
+      } while (seg_next(s, sched, p, share, cta));
       // every MMA issued so far finishes before tensor memory is freed
       if (elect_one()) tc_commit(&bars->drain[iss]);
       __syncwarp();
@@ -722,9 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp & 3;
     const int r = w * 32 + lane;
     const int grp = (warp - kWarpRebuild) >> 2;
-    if (u0 < u1) {
+    if (work) {
       Seg s;
-      seg_init(s, sched, p, u0, u1);
+      seg_init(s, sched, p, share, cta);
       // the groups take turns; with two matrices a group's tiles are all of
       // one (kGroups is even)
       constexpr int kStep = kGroups / NMAT;  // k-blocks from one tile of a group to the next
@@ -803,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring_next(ra, p.sa, kGroups);
         }
         skip = kb - n_kb;
-      } while (ok && seg_next(s, sched, p));
+      } while (ok && seg_next(s, sched, p, share, cta));
     }
   } else {
     // ------------------------------- epilogue -------------------------------
@@ -811,12 +854,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stream until it has completed
     griddep_wait();
     if (warp == kWarpEpi && lane == 0) griddep_launch_dependents();
-    if (u0 < u1) {
+    if (work) {
       const int w = warp & 3;  // TMEM lanes 32 w ..
       const int r = w * 32 + lane;
       const bool elected = warp == kWarpEpi && lane == 0;
       Seg s;
-      seg_init(s, sched, p, u0, u1);
+      seg_init(s, sched, p, share, cta);
       uint32_t seg = 0;
       int first_tile = 0;  // the segment's first tile in the CTA's sequence
       float* turn = reinterpret_cast<float*>(smem + p.turn_off) + w * 256;
@@ -864,13 +907,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
         } else {
           // part of a tile: contributors c_first..c_last
-          const int c_first = unit_owner(s.tile_u, total, grid);
-          const int c_last = unit_owner(s.tile_u + p.KB - 1, total, grid);
+          const int c_first = unit_owner(s.tile_u, share.sk_units, share.grid);
+          const int c_last = unit_owner(s.tile_u + p.KB - 1, share.sk_units, share.grid);
           const int n_contrib = c_last - c_first + 1;
           // contributor c's sums: its slot 0 when the tile opens its share,
           // else slot 1; [matrix][chunk][weight row][8 columns]
           auto part = [&](int c) -> float* {
-            const int which = units_before(c, total, grid) >= s.tile_u ? 0 : 1;
+            const int which = units_before(c, share.sk_units, share.grid) >= s.tile_u ? 0 : 1;
             return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
           };
           float* mine = part(cta);
@@ -902,13 +945,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               t.nvalid = s.nvalid;
               t.c_first = c_first;
               t.c_last = c_last;
-              t.first_slot = units_before(c_first, total, grid) >= s.tile_u ? 0 : 1;
+              t.first_slot = units_before(c_first, share.sk_units, share.grid) >= s.tile_u ? 0 : 1;
             }
           }
         }
         ++seg;
         first_tile += n_kb * NMAT;
-      } while (seg_next(s, sched, p));
+      } while (seg_next(s, sched, p, share, cta));
     }
   }
 

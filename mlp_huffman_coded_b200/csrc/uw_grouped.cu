@@ -125,6 +125,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
 // One lane of the warp, the same every time (a converged warp elects alike).
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred;
@@ -136,8 +142,14 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars* b, uint32_t* status) {
+// A warp's wait.  The polling loop stays out of line: with it inlined at every
+// wait the loops outgrow the instruction caches (decode products +5%).
+__device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, GBars* b, uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, &b->abort, status));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GBars* b, uint32_t* status) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_long(bar, parity, b, status);
 }
 
 // the 4 epilogue warps (named barrier 1)
@@ -792,13 +804,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&bars->wfull[rw.slot], rw.use & 1, bars, p.status);
           if (!ok) break;
           const uint32_t body = smem_s + p.w_base + static_cast<uint32_t>(rw.slot) * p.w_slot_bytes;
+          // verbatim rows: one mask bit per row, no per-element test
+          const uint32_t mw = lds32(body + kBodyMask + 4 * w);
           uint32_t o[32];
           if (uniform) rebuild_row(pal, true, body, r, o);
           else rebuild_row(pal, false, body, r, o);
-          // verbatim rows: one mask bit per row, no per-element test
-          const uint4 mk = lds128(body + kBodyMask);
-          const uint32_t mw = w == 0 ? mk.x : (w == 1 ? mk.y : (w == 2 ? mk.z : mk.w));
           if ((mw >> lane) & 1) {
+            const uint4 mk = lds128(body + kBodyMask);
             const int idx = (w > 0 ? __popc(mk.x) : 0) + (w > 1 ? __popc(mk.y) : 0) + (w > 2 ? __popc(mk.z) : 0) +
                             __popc(mw & ((1u << lane) - 1));
             if (idx < p.vcap) {

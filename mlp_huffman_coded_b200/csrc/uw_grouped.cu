@@ -109,13 +109,28 @@ struct Todo {
   int e, mt, slot0, nvalid, c_first, c_last, first_slot, pad;
 };
 
+// The tiles (group, row tile, column tile), column tiles of a row tile next to
+// each other, are dealt out in waves of one tile per CTA: CTAs that work at
+// the same time share weight tiles (the column tiles of a row tile) and
+// activation tiles through L2.  What does not fill waves evenly, between one
+// and two tiles per CTA (or everything, when there are fewer tiles), is cut
+// into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
+// instead read the weights of three column tiles three times from HBM: the
+// first CTA's second column tile came when L2 had long moved on.
+struct Share {
+  int grid, waves;        // CTAs that take part, whole tiles per CTA
+  int sk_each, sk_long;   // k-blocks of the tiles after the waves: lengths of the runs
+  int u0, u1;             // this CTA's run of them
+};
+
 struct GBars {
   uint64_t wfull[kMaxSlots], wempty[kMaxSlots];
   uint64_t xfull[kMaxSlots], xempty[kMaxSlots];
   uint64_t afull[kMaxSlots], aempty[kMaxSlots];
   uint64_t acc_full[2], acc_empty[2], drain[kMaxIssuers];
   uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
-  uint32_t tmem_base, abort, tiles, n_todo;
+  uint32_t tmem_base, abort, n_todo;
+  Share share;
   Todo todo[2];
 };
 
@@ -179,19 +194,6 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
 }
 
 // ------------------------------- schedule ------------------------------------
-// The tiles (group, row tile, column tile), column tiles of a row tile next to
-// each other, are dealt out in waves of one tile per CTA: CTAs that work at
-// the same time share weight tiles (the column tiles of a row tile) and
-// activation tiles through L2.  What does not fill waves evenly, between one
-// and two tiles per CTA (or everything, when there are fewer tiles), is cut
-// into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
-// instead read the weights of three column tiles three times from HBM: the
-// first CTA's second column tile came when L2 had long moved on.
-struct Share {
-  int grid, waves;  // CTAs that take part, whole tiles per CTA
-  int sk_units;     // k-blocks of the tiles after the waves
-  int u0, u1;       // this CTA's run of them
-};
 // A CTA's work as segments: runs of k-blocks of one tile.  Every role walks
 // the same sequence.
 struct Seg {
@@ -202,12 +204,14 @@ struct Seg {
   int tile_u;         // first k-block of the whole tile in the run's count
 };
 
-__device__ __forceinline__ int units_before(int c, int total, int grid) {
-  return static_cast<int>(static_cast<long long>(c) * total / grid);
-}
-// CTA whose run holds unit u
-__device__ __forceinline__ int unit_owner(int u, int total, int grid) {
-  return static_cast<int>((static_cast<long long>(u + 1) * grid - 1) / total);
+// Runs of the k-blocks: the first sk_long CTAs have one more than the others.
+__device__ __forceinline__ int units_before(int c, const Share& h) { return c * h.sk_each + min(c, h.sk_long); }
+// CTA whose run holds k-block u
+__device__ __forceinline__ int unit_owner(int u, const Share& h) {
+  const int in_long = h.sk_long * (h.sk_each + 1);
+  return u < in_long ? static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(h.sk_each + 1))
+                     : h.sk_long + static_cast<int>(static_cast<uint32_t>(u - in_long) /
+                                                    static_cast<uint32_t>(h.sk_each));
 }
 
 __device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) {
@@ -215,14 +219,16 @@ __device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) 
   // with fewer k-blocks than CTAs the last CTAs have none: every CTA that the
   // shares count has at least one
   h.grid = min(p.grid, tiles * p.KB);
-  h.waves = h.sk_units = h.u0 = h.u1 = 0;
+  h.waves = h.sk_each = h.sk_long = h.u0 = h.u1 = 0;
   if (cta >= h.grid) return h;
   const int full = tiles / h.grid, rest = tiles - full * h.grid;
   h.waves = rest && full ? full - 1 : full;
-  h.sk_units = (tiles - h.waves * h.grid) * p.KB;
-  if (h.sk_units) {
-    h.u0 = units_before(cta, h.sk_units, h.grid);
-    h.u1 = units_before(cta + 1, h.sk_units, h.grid);
+  const int units = (tiles - h.waves * h.grid) * p.KB;
+  if (units) {
+    h.sk_each = units / h.grid;
+    h.sk_long = units - h.sk_each * h.grid;
+    h.u0 = units_before(cta, h);
+    h.u1 = units_before(cta + 1, h);
   }
   return h;
 }
@@ -241,9 +247,13 @@ __device__ __forceinline__ void seg_fill(Seg& s, const SchedEntry* sched, const 
   }
   const SchedEntry en = sched[s.e];
   const int n_nt = en.n_nt >> 16;
-  const int local = tile - en.tile0;
-  s.mt = local / n_nt;
-  s.nt = local - s.mt * n_nt;
+  s.mt = tile - en.tile0;
+  s.nt = 0;
+  if (n_nt > 1) {
+    const int local = s.mt;
+    s.mt = static_cast<int>(static_cast<uint32_t>(local) / static_cast<uint32_t>(n_nt));
+    s.nt = local - s.mt * n_nt;
+  }
   s.ntile = en.n_nt & 0xFFFF;
   s.slot0 = en.start + s.nt * s.ntile;
   s.nvalid = min(s.ntile, en.count - s.nt * s.ntile);
@@ -254,7 +264,7 @@ __device__ __forceinline__ void seg_here(Seg& s, const SchedEntry* sched, const 
     s.kb1 = p.KB;
     seg_fill(s, sched, p, s.wave * h.grid + cta);
   } else {
-    const int tile = s.u / p.KB;
+    const int tile = static_cast<int>(static_cast<uint32_t>(s.u) / static_cast<uint32_t>(p.KB));
     s.kb0 = s.u - tile * p.KB;
     s.kb1 = min(p.KB, s.kb0 + (h.u1 - s.u));
     s.tile_u = s.u - s.kb0;
@@ -352,6 +362,8 @@ __device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
 // ------------------------------- epilogue ------------------------------------
 // FP32 throughout; the only rounding is the store's.  The GELU forms are
 // written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
+// Divisions are the fast ones (2 units in the last place; 0 where exp
+// overflows the range, as the limit is).
 // SiLU(v) for a product that is rounded to BF16 next: the fast exponential
 // (relative error about 2^-24 (2 + 1.2 |v|), far below BF16's 2^-9 wherever
 // the result is not negligible) and the fast division (2 units in the last
@@ -373,12 +385,12 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float t = 1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]);  // 2 sqrt(2 / pi) (...)
-        v[j] = v[j] / (1.0f + expf(-t));
+        v[j] = __fdividef(v[j], 1.0f + expf(-t));
       }
       break;
     case UW_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = v[j] / (1.0f + expf(-v[j]));
+      for (int j = 0; j < N; ++j) v[j] = __fdividef(v[j], 1.0f + expf(-v[j]));
       break;
     default: break;
   }
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       if (bad) record_status(p.status, UW_ERR_INVALID_ARG);
       sched[p.E].tile0 = bad ? 0 : base;
-      bars->tiles = bad ? 0 : base;
+      bars->share = share_of(static_cast<int>(blockIdx.x), bad ? 0 : base, p);
     }
   }
   tc_fence_before();
@@ -567,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const int cta = static_cast<int>(blockIdx.x);
-  const Share share = share_of(cta, static_cast<int>(bars->tiles), p);
+  const Share& share = bars->share;
   const bool work = share.waves > 0 || share.u0 < share.u1;
   auto desc = [&](int m, int e) -> const ExpertDesc* { return p.table[m] ? p.table[m] + e : &p.one; };
 
@@ -609,14 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n = min(kSpan, s.kb1 - kb) * NMAT;
           for (int i0 = 0; i0 < n; i0 += kWBatch) {
             const int j = (i0 + lane) / NMAT;  // k-block of this lane's tile
-            uint32_t a = __shfl_sync(0xFFFFFFFFu, v0, j & 31), b = __shfl_sync(0xFFFFFFFFu, v0, (j + 1) & 31);
-            if constexpr (NMAT == 2) {
-              const uint32_t a1 = __shfl_sync(0xFFFFFFFFu, v1, j & 31), b1 = __shfl_sync(0xFFFFFFFFu, v1, (j + 1) & 31);
-              if (m) {
-                a = a1;
-                b = b1;
-              }
-            }
             const int count = min(kWBatch, n - i0);
             Ring mine = rw;
             ring_next(mine, p.sw, lane & (kWBatch - 1));
@@ -626,17 +630,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, good);
             if (!ok) break;
             if (lane < count) {
+              // the record first: it does not wait for the offsets to arrive
+              uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(mine.slot) * p.w_slot_bytes;
+              uint64_t* bar = &bars->wfull[mine.slot];
+              const uint8_t* src = pack + static_cast<uint64_t>(kb + j) * kBody;
+              mbar_expect_tx(bar, kBody);
+              if (reread) bulk_load(slot, src, kBody, bar);
+              else bulk_load_hint(slot, src, kBody, bar, once);
+            }
+            uint32_t a = __shfl_sync(0xFFFFFFFFu, v0, j & 31), b = __shfl_sync(0xFFFFFFFFu, v0, (j + 1) & 31);
+            if constexpr (NMAT == 2) {
+              const uint32_t a1 = __shfl_sync(0xFFFFFFFFu, v1, j & 31), b1 = __shfl_sync(0xFFFFFFFFu, v1, (j + 1) & 31);
+              if (m) {
+                a = a1;
+                b = b1;
+              }
+            }
+            if (lane < count) {
               uint32_t rows = 0;
               if (b < a || b - a > 128u || b > n_verb) record_status(p.status, UW_ERR_CORRUPT);
               else rows = min(b - a, static_cast<uint32_t>(p.vcap));
-              uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(mine.slot) * p.w_slot_bytes;
-              uint64_t* bar = &bars->wfull[mine.slot];
               bars->tail_first[mine.slot] = a;
-              mbar_arrive_expect_tx(bar, kBody + rows * 128u);
-              const uint8_t* src = pack + static_cast<uint64_t>(kb + j) * kBody;
-              if (reread) bulk_load(slot, src, kBody, bar);
-              else bulk_load_hint(slot, src, kBody, bar, once);
-              if (rows) bulk_load(slot + kBody, tails + static_cast<uint64_t>(a) * 128u, rows * 128u, bar);
+              mbar_arrive_expect_tx(&bars->wfull[mine.slot], rows * 128u);
+              if (rows)
+                bulk_load(smem + p.w_base + static_cast<uint32_t>(mine.slot) * p.w_slot_bytes + kBody,
+                          tails + static_cast<uint64_t>(a) * 128u, rows * 128u, &bars->wfull[mine.slot]);
             }
             __syncwarp();
             issued += count;
@@ -919,13 +937,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
         } else {
           // part of a tile: contributors c_first..c_last
-          const int c_first = unit_owner(s.tile_u, share.sk_units, share.grid);
-          const int c_last = unit_owner(s.tile_u + p.KB - 1, share.sk_units, share.grid);
+          const int c_first = unit_owner(s.tile_u, share);
+          const int c_last = unit_owner(s.tile_u + p.KB - 1, share);
           const int n_contrib = c_last - c_first + 1;
           // contributor c's sums: its slot 0 when the tile opens its share,
           // else slot 1; [matrix][chunk][weight row][8 columns]
           auto part = [&](int c) -> float* {
-            const int which = units_before(c, share.sk_units, share.grid) >= s.tile_u ? 0 : 1;
+            const int which = units_before(c, share) >= s.tile_u ? 0 : 1;
             return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
           };
           float* mine = part(cta);
@@ -957,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               t.nvalid = s.nvalid;
               t.c_first = c_first;
               t.c_last = c_last;
-              t.first_slot = units_before(c_first, share.sk_units, share.grid) >= s.tile_u ? 0 : 1;
+              t.first_slot = units_before(c_first, share) >= s.tile_u ? 0 : 1;
             }
           }
         }

@@ -123,6 +123,16 @@ struct Share {
   int u0, u1;             // this CTA's run of them
 };
 
+// A CTA's work as segments: runs of k-blocks of one tile.  Every role walks
+// the same sequence.
+struct Seg {
+  int wave, u;        // waves done, next k-block of the run
+  int e, mt, nt;
+  int kb0, kb1;
+  int ntile, slot0, nvalid;
+  int tile_u;         // first k-block of the whole tile in the run's count
+};
+
 struct GBars {
   uint64_t wfull[kMaxSlots], wempty[kMaxSlots];
   uint64_t xfull[kMaxSlots], xempty[kMaxSlots];
@@ -131,6 +141,8 @@ struct GBars {
   uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
   uint32_t tmem_base, abort, n_todo;
   Share share;
+  Seg first;
+  ExpertDesc desc[2];  // the first segment's matrices
   Todo todo[2];
 };
 
@@ -144,6 +156,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+
+// Takes a ticket: releases this thread's writes and those of the threads it
+// has met at a CTA barrier, and acquires what earlier tickets released.
+__device__ __forceinline__ uint32_t ticket(uint32_t* p) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
 }
 
 // One lane of the warp, the same every time (a converged warp elects alike).
@@ -194,24 +214,29 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
 }
 
 // ------------------------------- schedule ------------------------------------
-// A CTA's work as segments: runs of k-blocks of one tile.  Every role walks
-// the same sequence.
-struct Seg {
-  int wave, u;        // waves done, next k-block of the run
-  int e, mt, nt;
-  int kb0, kb1;
-  int ntile, slot0, nvalid;
-  int tile_u;         // first k-block of the whole tile in the run's count
-};
+
+// a / b for 0 <= a, 0 < b, from the approximate quotient: the set-up is a
+// chain of divisions, and the exact one takes 40 instructions.
+__device__ __forceinline__ int quick_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  int r = a - q * b;
+  while (r < 0) {
+    --q;
+    r += b;
+  }
+  while (r >= b) {
+    ++q;
+    r -= b;
+  }
+  return q;
+}
 
 // Runs of the k-blocks: the first sk_long CTAs have one more than the others.
 __device__ __forceinline__ int units_before(int c, const Share& h) { return c * h.sk_each + min(c, h.sk_long); }
 // CTA whose run holds k-block u
 __device__ __forceinline__ int unit_owner(int u, const Share& h) {
   const int in_long = h.sk_long * (h.sk_each + 1);
-  return u < in_long ? static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(h.sk_each + 1))
-                     : h.sk_long + static_cast<int>(static_cast<uint32_t>(u - in_long) /
-                                                    static_cast<uint32_t>(h.sk_each));
+  return u < in_long ? quick_div(u, h.sk_each + 1) : h.sk_long + quick_div(u - in_long, h.sk_each);
 }
 
 __device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) {
@@ -221,11 +246,11 @@ __device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) 
   h.grid = min(p.grid, tiles * p.KB);
   h.waves = h.sk_each = h.sk_long = h.u0 = h.u1 = 0;
   if (cta >= h.grid) return h;
-  const int full = tiles / h.grid, rest = tiles - full * h.grid;
+  const int full = quick_div(tiles, h.grid), rest = tiles - full * h.grid;
   h.waves = rest && full ? full - 1 : full;
   const int units = (tiles - h.waves * h.grid) * p.KB;
   if (units) {
-    h.sk_each = units / h.grid;
+    h.sk_each = quick_div(units, h.grid);
     h.sk_long = units - h.sk_each * h.grid;
     h.u0 = units_before(cta, h);
     h.u1 = units_before(cta + 1, h);
@@ -251,7 +276,7 @@ __device__ __forceinline__ void seg_fill(Seg& s, const SchedEntry* sched, const 
   s.nt = 0;
   if (n_nt > 1) {
     const int local = s.mt;
-    s.mt = static_cast<int>(static_cast<uint32_t>(local) / static_cast<uint32_t>(n_nt));
+    s.mt = quick_div(local, n_nt);
     s.nt = local - s.mt * n_nt;
   }
   s.ntile = en.n_nt & 0xFFFF;
@@ -264,7 +289,7 @@ __device__ __forceinline__ void seg_here(Seg& s, const SchedEntry* sched, const 
     s.kb1 = p.KB;
     seg_fill(s, sched, p, s.wave * h.grid + cta);
   } else {
-    const int tile = static_cast<int>(static_cast<uint32_t>(s.u) / static_cast<uint32_t>(p.KB));
+    const int tile = quick_div(s.u, p.KB);
     s.kb0 = s.u - tile * p.KB;
     s.kb1 = min(p.KB, s.kb0 + (h.u1 - s.u));
     s.tile_u = s.u - s.kb0;
@@ -507,34 +532,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   // ---- set-up: barriers, tensor memory and the table of tiles
-  if (warp == kWarpW && lane == 0) {
-    for (int s = 0; s < p.sw; ++s) {
-      mbar_init(&bars->wfull[s], 1);
-      mbar_init(&bars->wempty[s], 4);
-    }
-    for (int s = 0; s < p.sx; ++s) {
-      mbar_init(&bars->xfull[s], 1);
-      mbar_init(&bars->xempty[s], NMAT);
-    }
-    for (int s = 0; s < p.sa; ++s) {
-      mbar_init(&bars->afull[s], 4);
-      mbar_init(&bars->aempty[s], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->acc_full[i], p.n_iss);
-      mbar_init(&bars->acc_empty[i], 4);
-    }
-    for (int i = 0; i < kMaxIssuers; ++i) mbar_init(&bars->drain[i], 1);
-    bars->abort = 0;
-    bars->n_todo = 0;
-    mbar_fence_init();
+  const int cta = static_cast<int>(blockIdx.x);
+  auto desc = [&](int m, int e) -> const ExpertDesc* { return p.table[m] ? p.table[m] + e : &p.one; };
+  if (warp == kWarpMma) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
   } else if (warp == kWarpX && lane == 0) {
     prefetch_tensormap(&tm_x);
     if (!p.gather) prefetch_tensormap(&tm_x64);
-  } else if (warp == kWarpMma) {
-    tmem_alloc(&bars->tmem_base, kTmemCols);
-    tmem_relinquish();
-  } else if (warp == kWarpEpi) {
+  } else if (warp == kWarpW) {
+    if (lane < p.sw) {
+      mbar_init(&bars->wfull[lane], 1);
+      mbar_init(&bars->wempty[lane], 4);
+    }
+    if (lane < p.sx) {
+      mbar_init(&bars->xfull[lane], 1);
+      mbar_init(&bars->xempty[lane], NMAT);
+    }
+    if (lane < p.sa) {
+      mbar_init(&bars->afull[lane], 4);
+      mbar_init(&bars->aempty[lane], 1);
+    }
+    if (lane < 2) {
+      mbar_init(&bars->acc_full[lane], p.n_iss);
+      mbar_init(&bars->acc_empty[lane], 4);
+    }
+    if (lane < kMaxIssuers) mbar_init(&bars->drain[lane], 1);
+    if (lane == 0) {
+      bars->abort = 0;
+      bars->n_todo = 0;
+    }
+    mbar_fence_init();
+    __syncwarp();
     if (!p.early) griddep_wait();
     int base = 0;
     bool bad = false;
@@ -548,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // offsets that leave [0, n_rows] or fall: nothing is computed
       bad |= a < 0 || b < a || b > p.n_rows;
       const int cnt = bad ? 0 : b - a;
-      const int n_nt = (cnt + p.cap - 1) / p.cap;
-      const int ntile = n_nt ? ((cnt + n_nt - 1) / n_nt + 15) / 16 * 16 : 16;
+      const int n_nt = cnt <= p.cap ? min(cnt, 1) : quick_div(cnt + p.cap - 1, p.cap);
+      const int each = n_nt > 1 ? quick_div(cnt + n_nt - 1, n_nt) : cnt;
+      const int ntile = max(16, (each + 15) & ~15);
       const int tiles = n_nt * p.n_mt;
       int incl = tiles;
 #pragma unroll
@@ -567,21 +597,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       base += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+      if (lane == 0) record_status(p.status, UW_ERR_INVALID_ARG);
+      base = 0;
+    }
+    if (lane == 0) sched[p.E].tile0 = base;
+    __syncwarp();
+    // this CTA's share and its first segment, found once for every role
+    const Share h = share_of(cta, base, p);
+    Seg s;
+    if (h.waves > 0 || h.u0 < h.u1) {
+      seg_init(s, sched, p, h, cta);
+      // its matrices' records for every role, and the tile records of the
+      // first batch
+      constexpr int kDescs = NMAT == 2 && !PAIR ? 2 : 1;
+      constexpr int kWords = sizeof(ExpertDesc) / 16;
+      if (lane < kDescs * kWords)
+        reinterpret_cast<uint4*>(bars->desc)[lane] =
+            reinterpret_cast<const uint4*>(desc(lane / kWords, s.e))[lane % kWords];
+      __syncwarp();
+      if (lane < min(kWBatch, (s.kb1 - s.kb0) * NMAT)) {
+        const int m = NMAT == 2 ? lane & 1 : 0;
+        const uint8_t* src = bars->desc[PAIR ? 0 : m].pack +
+                             (static_cast<uint64_t>(row_tile<PAIR>(p, s.mt, m)) * p.KB + s.kb0 + lane / NMAT) * kBody;
+        mbar_expect_tx(&bars->wfull[lane], kBody);
+        bulk_load(smem + p.w_base + static_cast<uint32_t>(lane) * p.w_slot_bytes, src, kBody, &bars->wfull[lane]);
+      }
+    }
     if (lane == 0) {
-      if (bad) record_status(p.status, UW_ERR_INVALID_ARG);
-      sched[p.E].tile0 = bad ? 0 : base;
-      bars->share = share_of(static_cast<int>(blockIdx.x), bad ? 0 : base, p);
+      bars->share = h;
+      bars->first = s;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int cta = static_cast<int>(blockIdx.x);
   const Share& share = bars->share;
   const bool work = share.waves > 0 || share.u0 < share.u1;
-  auto desc = [&](int m, int e) -> const ExpertDesc* { return p.table[m] ? p.table[m] + e : &p.one; };
+  const int first_e = bars->first.e;
+  auto matrix = [&](int m, int e) -> const ExpertDesc* { return e == first_e ? &bars->desc[m] : desc(m, e); };
 
   if (warp == kWarpW) {
     // --------------------------- weight producer ----------------------------
@@ -592,16 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kSpan = 28;  // k-blocks per set of offsets: whole batches, and one offset more
     if (work) {
       const uint64_t once = l2_evict_first();
-      Seg s;
-      seg_init(s, sched, p, share, cta);
+      Seg s = bars->first;
       Ring rw{0, 0};
       int issued = 0;
       bool ok = true;
       const int m = NMAT == 2 ? lane & 1 : 0;  // this lane's matrix
       do {
         // lane l: offset of tile kb + l
-        const ExpertDesc* d0 = desc(0, s.e);
-        const ExpertDesc* d1 = NMAT == 2 && !PAIR ? desc(1, s.e) : d0;
+        const ExpertDesc* d0 = matrix(0, s.e);
+        const ExpertDesc* d1 = NMAT == 2 && !PAIR ? matrix(1, s.e) : d0;
         const int64_t t0 = static_cast<int64_t>(row_tile<PAIR>(p, s.mt, 0)) * p.KB;
         const int64_t t1 = static_cast<int64_t>(row_tile<PAIR>(p, s.mt, 1)) * p.KB;
         const uint32_t* off0 = d0->pack_off + t0 + lane;
@@ -629,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               good = mbar_wait(&bars->wempty[mine.slot], (mine.use - 1) & 1, &bars->abort, p.status);
             ok = __all_sync(0xFFFFFFFFu, good);
             if (!ok) break;
-            if (lane < count) {
+            if (lane < count && issued > 0) {  // (the first batch's are on their way)
               // the record first: it does not wait for the offsets to arrive
               uint8_t* slot = smem + p.w_base + static_cast<uint32_t>(mine.slot) * p.w_slot_bytes;
               uint64_t* bar = &bars->wfull[mine.slot];
@@ -675,8 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------- activation producer --------------------------
     if (work) {
       griddep_wait();
-      Seg s;
-      seg_init(s, sched, p, share, cta);
+      Seg s = bars->first;
       Ring rx{0, 0};
       int issued = 0;
       bool ok = true;
@@ -729,8 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop and one elected lane issues: with uniform
     // control flow the operands stay in uniform registers.
     if (iss < p.n_iss && work) {
-      Seg s;
-      seg_init(s, sched, p, share, cta);
+      Seg s = bars->first;
       // with two matrices issuer m has matrix m's tile of every k-block; with
       // one, the issuers take turns
       const int per = p.n_iss / NMAT, kstep = NMAT * per;
@@ -796,8 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = w * 32 + lane;
     const int grp = (warp - kWarpRebuild) >> 2;
     if (work) {
-      Seg s;
-      seg_init(s, sched, p, share, cta);
+      Seg s = bars->first;
       // the groups take turns; with two matrices a group's tiles are all of
       // one (kGroups is even)
       constexpr int kStep = kGroups / NMAT;  // k-blocks from one tile of a group to the next
@@ -810,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = tmem + (static_cast<uint32_t>(w * 32) << 16) + p.a_col0;
       do {
         if (cur_e != s.e) {
-          const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
+          const ExpertDesc* d = matrix(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
           pal = load_palette(d);
           uniform = d->mixed == 0;
           cur_e = s.e;
@@ -842,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
               // more verbatim rows than staged ones: from HBM
-              const ExpertDesc* d = desc(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
+              const ExpertDesc* d = matrix(NMAT == 2 && !PAIR ? grp & 1 : 0, s.e);
               const uint64_t g = static_cast<uint64_t>(bars->tail_first[rw.slot]) + idx;
               if (g < d->n_verbatim) {
                 const uint4* src = reinterpret_cast<const uint4*>(d->tails + g * 128u);
@@ -888,8 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w = warp & 3;  // TMEM lanes 32 w ..
       const int r = w * 32 + lane;
       const bool elected = warp == kWarpEpi && lane == 0;
-      Seg s;
-      seg_init(s, sched, p, share, cta);
+      Seg s = bars->first;
       uint32_t seg = 0;
       int first_tile = 0;  // the segment's first tile in the CTA's sequence
       float* turn = reinterpret_cast<float*>(smem + p.turn_off) + w * 256;
@@ -964,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           group_sync();  // every store of the group precedes the ticket
           if (elected) {
             // a CTA opens at most one tile that others finish: its counter
-            const bool last = atom_add_acq_rel_gpu(p.counters + c_first, 1u) == static_cast<uint32_t>(n_contrib - 1);
+            const bool last = ticket(p.counters + c_first) == static_cast<uint32_t>(n_contrib - 1);
             if (last) p.counters[c_first] = 0;  // all have arrived: ready for the next launch
             if (last) {
               // every warp of the CTA adds the parts up once the roles are done

@@ -673,6 +673,7 @@ class Route:
         self.rows = torch.empty(n_tokens * top_k, dtype=torch.int32, device=device)
         self.offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=device)
         self.device = self.weights.get_device()
+        self.addresses = tuple(t.data_ptr() for t in (self.weights, self.experts, self.slots, self.rows, self.offsets))
 
 
 def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:
@@ -685,8 +686,7 @@ def moe_route(logits, route: Route, ws: Workspace, renormalize: bool = True, str
     typ, types = _out_type(logits, "logits")
     lp = _tensor(logits, "logits", types, (route.n_tokens, route.n_experts), route.device)
     _call("uw_moe_route", route.device, stream, lp, typ, route.n_tokens, route.n_experts,
-          route.top_k, int(renormalize), route.weights.data_ptr(), route.experts.data_ptr(), route.slots.data_ptr(),
-          route.rows.data_ptr(), route.offsets.data_ptr(), *_space(ws, route.device))
+          route.top_k, int(renormalize), *route.addresses, *_space(ws, route.device))
 
 
 def moe_combine(parts, slots, weights, y, residual=None, stream=None):

@@ -113,9 +113,8 @@ struct Todo {
 // The tiles (group, row tile, column tile), column tiles of a row tile next to
 // each other, are dealt out in waves of one tile per CTA: CTAs that work at
 // the same time share weight tiles (the column tiles of a row tile) and
-// activation tiles through L2.  What does not fill waves evenly, between one
-// and two tiles per CTA (or everything, when there are fewer tiles), is cut
-// into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
+// activation tiles through L2.  What does not fill waves evenly (up to two
+// tiles per CTA) is cut into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
 // instead read the weights of three column tiles three times from HBM: the
 // first CTA's second column tile came when L2 had long moved on.
 struct Share {
@@ -240,7 +239,8 @@ __device__ __forceinline__ int unit_owner(int u, const Share& h) {
   return u < in_long ? quick_div(u, h.sk_each + 1) : h.sk_long + quick_div(u - in_long, h.sk_each);
 }
 
-__device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) {
+// wide: some group has more than one column tile
+__device__ __forceinline__ Share share_of(int cta, int tiles, bool wide, const GParams& p) {
   Share h;
   // with fewer k-blocks than CTAs the last CTAs have none: every CTA that the
   // shares count has at least one
@@ -248,13 +248,20 @@ __device__ __forceinline__ Share share_of(int cta, int tiles, const GParams& p) 
   h.waves = h.sk_each = h.sk_long = h.u0 = h.u1 = 0;
   if (cta >= h.grid) return h;
   const int full = quick_div(tiles, h.grid), rest = tiles - full * h.grid;
-  h.waves = rest && full ? full - 1 : full;
+  // The run of the last, partial wave is long enough to be worth joining
+  // alone only when it is some k-blocks long; then a wave more leaves fewer
+  // column tiles apart in time from those they share weights with.  (8 x 512
+  // rows of 4096 x 14336: 568 us with runs of 1.6 tiles, 487 with runs of 0.6
+  // after the waves; without column tiles to share with, 1 row of 8 experts,
+  // 59.5 against 62.1.)
+  const bool wave_more = wide && rest * p.KB >= 2 * p.join * h.grid;
+  h.waves = rest && full && !wave_more ? full - 1 : full;
   const int units = (tiles - h.waves * h.grid) * p.KB;
   // The last tiles are shared out only where that saves more k-blocks than
   // joining the parts costs
   if (units <= h.grid * p.KB && p.KB <= quick_div(units, h.grid) + p.join) {
     h.waves += cta < tiles - h.waves * h.grid ? 1 : 0;
-  } else if (rest && full && 2 * p.KB <= quick_div(units, h.grid) + p.join) {
+  } else if (h.waves < full && 2 * p.KB <= quick_div(units, h.grid) + p.join) {
     h.waves = full + (cta < rest ? 1 : 0);
   } else if (units) {
     h.sk_each = quick_div(units, h.grid);
@@ -573,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (!p.early) griddep_wait();
     int base = 0;
-    bool bad = false;
+    bool bad = false, wide = false;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int a = 0, b = 0;
@@ -588,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int each = n_nt > 1 ? quick_div(cnt + n_nt - 1, n_nt) : cnt;
       const int ntile = max(16, (each + 15) & ~15);
       const int tiles = n_nt * p.n_mt;
+      wide |= n_nt > 1;
       int incl = tiles;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) sched[p.E].tile0 = base;
     __syncwarp();
     // this CTA's share and its first segment, found once for every role
-    const Share h = share_of(cta, base, p);
+    const Share h = share_of(cta, base, __any_sync(0xFFFFFFFFu, wide), p);
     Seg s;
     if (h.waves > 0 || h.u0 < h.u1) {
       seg_init(s, sched, p, h, cta);

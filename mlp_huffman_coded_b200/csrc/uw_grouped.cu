@@ -44,6 +44,7 @@
 //  * Barrier waits are bounded: a timeout records UW_ERR_TIMEOUT, drains
 //    copies and MMAs in flight, frees tensor memory and returns.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -447,14 +448,24 @@ __device__ __forceinline__ void load_bias(const GParams& p, int e, int mt, int r
   }
 }
 
-// Values of matrix row n for slots slot0 + 8 cc ..: activation, residual,
-// store.  Where rows of y start on 16 bytes the warp turns its 32 x 8 values
-// around in shared memory (`turn`, 1 KB of its own), so that a lane stores 8
-// consecutive ones.
-__device__ __forceinline__ void store8(const GParams& p, float (&v)[8], int cc, int n, int slot0, int nvalid,
-                                       float* turn) {
+// Where rows of y start on 16 bytes (p.vec) a warp turns its 32 rows x 8 slots
+// around in shared memory and lane l stores 8 consecutive values of slot
+// l / 4, rows 8 (l % 4) ..: the index of the first one, or -1.
+__device__ __forceinline__ int64_t turned_index(const GParams& p, int cc, int n, int slot0, int nvalid) {
   const int lane = threadIdx.x & 31;
-  const int cols = nvalid - cc * 8;
+  const int n0 = n - lane + (lane & 3) * 8;
+  return (lane >> 2) < nvalid - cc * 8 && n0 < p.N ? static_cast<int64_t>(slot0 + cc * 8 + (lane >> 2)) * p.N + n0 : -1;
+}
+// The residual of those 8 values, asked for ahead of the sums it is added to.
+__device__ __forceinline__ uint4 turned_residual(const GParams& p, int64_t i) {
+  return i >= 0 ? *reinterpret_cast<const uint4*>(p.residual + i) : make_uint4(0, 0, 0, 0);
+}
+
+// Values of matrix row n for slots slot0 + 8 cc ..: residual, store.  `turn`:
+// 1 KB of the warp's own.
+__device__ __forceinline__ void store8(const GParams& p, float (&v)[8], int cc, int n, int slot0, int nvalid,
+                                       const uint4& residual, float* turn) {
+  const int lane = threadIdx.x & 31;
   if (p.vec) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) turn[j * 32 + lane] = v[j];
@@ -462,13 +473,11 @@ __device__ __forceinline__ void store8(const GParams& p, float (&v)[8], int cc, 
     const float4 q0 = *reinterpret_cast<const float4*>(turn + lane * 8);
     const float4 q1 = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
     __syncwarp();
-    const int n0 = n - lane + (lane & 3) * 8;  // lane l: slot l / 4, rows 8 (l % 4) ..
-    if ((lane >> 2) >= cols || n0 >= p.N) return;
+    const int64_t i = turned_index(p, cc, n, slot0, nvalid);
+    if (i < 0) return;
     float f[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-    const int64_t i = static_cast<int64_t>(slot0 + cc * 8 + (lane >> 2)) * p.N + n0;
     if (p.residual) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p.residual + i);
-      const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+      const uint32_t w4[4] = {residual.x, residual.y, residual.z, residual.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f[2 * j] += __uint_as_float(w4[j] << 16);
@@ -490,27 +499,50 @@ __device__ __forceinline__ void store8(const GParams& p, float (&v)[8], int cc, 
     }
     return;
   }
-  if (n >= p.N) return;
-  int64_t i = static_cast<int64_t>(slot0 + cc * 8) * p.N + n;
-#pragma unroll 1
-  for (int j = 0; j < 8 && j < cols; ++j, i += p.N) {
-    float f = v[0];
+  // a lane's own row: 32 consecutive values of a slot per warp
+  const int cols = n < p.N ? nvalid - cc * 8 : 0;
+  const int64_t i = static_cast<int64_t>(slot0 + cc * 8) * p.N + n;
+  if (p.residual) {
+    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.residual) + i;
+    __nv_bfloat16 r[8];
 #pragma unroll
-    for (int q = 1; q < 8; ++q) f = j == q ? v[q] : f;
-    if (p.residual) f += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.residual)[i]);
-    if (p.out_fp32) static_cast<float*>(p.y)[i] = f;
-    else static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(f);
+    for (int j = 0; j < 8; ++j) r[j] = j < cols ? src[static_cast<int64_t>(j) * p.N] : __nv_bfloat16();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += __bfloat162float(r[j]);
+  }
+  if (p.out_fp32) {
+    float* dst = static_cast<float*>(p.y) + i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < cols) dst[static_cast<int64_t>(j) * p.N] = v[j];
+  } else {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.y) + i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < cols) dst[static_cast<int64_t>(j) * p.N] = __float2bfloat16_rn(v[j]);
+  }
+}
+
+// The residuals of eight columns of a tile.
+template <int NMAT, bool PAIR>
+__device__ __forceinline__ void load_residual(const GParams& p, int cc, int mt, int slot0, int nvalid, int r,
+                                              uint4 (&res)[NMAT]) {
+#pragma unroll
+  for (int m = 0; m < NMAT; ++m) {
+    res[m] = make_uint4(0, 0, 0, 0);
+    if ((NMAT == 1 || PAIR) && p.vec && p.residual)
+      res[m] = turned_residual(p, turned_index(p, cc, (PAIR ? 2 * mt + m : mt) * 128 + r, slot0, nvalid));
   }
 }
 
 // Eight columns of a tile: the sums of its matrices (row r of the tile) to y.
 template <int NMAT, bool PAIR>
 __device__ __forceinline__ void emit(const GParams& p, float (&a)[NMAT][8], int cc, int mt, int slot0, int nvalid,
-                                     int r, const float (&bias)[NMAT], float* turn) {
+                                     int r, const float (&bias)[NMAT], const uint4 (&res)[NMAT], float* turn) {
   if constexpr (NMAT == 2 && !PAIR) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[0][j] = silu_fast(a[0][j]) * a[1][j];
-    store8(p, a[0], cc, mt * 128 + r, slot0, nvalid, turn);
+    store8(p, a[0], cc, mt * 128 + r, slot0, nvalid, res[0], turn);
   } else {
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) {
@@ -519,7 +551,7 @@ __device__ __forceinline__ void emit(const GParams& p, float (&a)[NMAT][8], int 
         for (int j = 0; j < 8; ++j) a[m][j] += bias[m];
       }
       activate(a[m], p.act);
-      store8(p, a[m], cc, (PAIR ? 2 * mt + m : mt) * 128 + r, slot0, nvalid, turn);
+      store8(p, a[m], cc, (PAIR ? 2 * mt + m : mt) * 128 + r, slot0, nvalid, res[m], turn);
     }
   }
 }
@@ -994,8 +1026,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int cc = 0; cc < n_chunks; ++cc) {
             float a[NMAT][8];
+            uint4 res[NMAT];
+            load_residual<NMAT, PAIR>(p, cc, s.mt, s.slot0, s.nvalid, r, res);
             own_sums(cc, a);
-            emit<NMAT, PAIR>(p, a, cc, s.mt, s.slot0, s.nvalid, r, bias, turn);
+            emit<NMAT, PAIR>(p, a, cc, s.mt, s.slot0, s.nvalid, r, bias, res, turn);
           }
           tc_fence_before();
           __syncwarp();
@@ -1006,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_last = unit_owner(s.tile_u + p.KB - 1, share);
           const int n_contrib = c_last - c_first + 1;
           // contributor c's sums: its slot 0 when the tile opens its share,
-          // else slot 1; [matrix][chunk][weight row][8 columns]
+          // else slot 1; [matrix][chunk of 8 columns][half][weight row][4 columns]
           auto part = [&](int c) -> float* {
             const int which = units_before(c, share) >= s.tile_u ? 0 : 1;
             return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
@@ -1018,9 +1052,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             own_sums(cc, a);
 #pragma unroll
             for (int m = 0; m < NMAT; ++m) {
-              float4* dst = reinterpret_cast<float4*>(mine + ((m * n_chunks + cc) * 128 + r) * 8);
+              float4* dst = reinterpret_cast<float4*>(mine) + (m * n_chunks + cc) * 256 + r;
               __stcg(dst, make_float4(a[m][0], a[m][1], a[m][2], a[m][3]));
-              __stcg(dst + 1, make_float4(a[m][4], a[m][5], a[m][6], a[m][7]));
+              __stcg(dst + 128, make_float4(a[m][4], a[m][5], a[m][6], a[m][7]));
             }
           }
           tc_fence_before();
@@ -1066,38 +1100,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     float bias[NMAT];
     load_bias<NMAT, PAIR>(p, t.e, t.mt, r, bias);
     float* turn = reinterpret_cast<float*>(smem) + warp * 256;
-    const float* first = p.partials + (2 * static_cast<int64_t>(t.c_first) + t.first_slot) * p.partial_stride;
 #pragma unroll 1
     for (int cc = warp >> 2; cc < n_chunks; cc += kThreads / 128) {
       float a[NMAT][8];
+      uint4 res[NMAT];
+      load_residual<NMAT, PAIR>(p, cc, t.mt, t.slot0, t.nvalid, r, res);
 #pragma unroll
       for (int m = 0; m < NMAT; ++m) {
-        const int64_t at = (static_cast<int64_t>(m * n_chunks + cc) * 128 + r) * 8;
-        const float4* src = reinterpret_cast<const float4*>(first + at);
-        const float4 f0 = __ldcg(src), f1 = __ldcg(src + 1);
-        a[m][0] = f0.x;
-        a[m][1] = f0.y;
-        a[m][2] = f0.z;
-        a[m][3] = f0.w;
-        a[m][4] = f1.x;
-        a[m][5] = f1.y;
-        a[m][6] = f1.z;
-        a[m][7] = f1.w;
-#pragma unroll 4
-        for (int c = t.c_first + 1; c <= t.c_last; ++c) {
-          src = reinterpret_cast<const float4*>(p.partials + 2 * static_cast<int64_t>(c) * p.partial_stride + at);
-          const float4 v0 = __ldcg(src), v1 = __ldcg(src + 1);
-          a[m][0] += v0.x;
-          a[m][1] += v0.y;
-          a[m][2] += v0.z;
-          a[m][3] += v0.w;
-          a[m][4] += v1.x;
-          a[m][5] += v1.y;
-          a[m][6] += v1.z;
-          a[m][7] += v1.w;
+        // contributors in CTA order, the loads of two in flight
+        const int64_t at = static_cast<int64_t>(m * n_chunks + cc) * 256 + r;
+        auto part = [&](int c) -> const float4* {
+          const int64_t slot = 2 * static_cast<int64_t>(c) + (c == t.c_first ? t.first_slot : 0);
+          return reinterpret_cast<const float4*>(p.partials + slot * p.partial_stride) + at;
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[m][j] = 0.0f;
+        auto add = [&](const float4& lo, const float4& hi) {
+          a[m][0] += lo.x;
+          a[m][1] += lo.y;
+          a[m][2] += lo.z;
+          a[m][3] += lo.w;
+          a[m][4] += hi.x;
+          a[m][5] += hi.y;
+          a[m][6] += hi.z;
+          a[m][7] += hi.w;
+        };
+#pragma unroll 1
+        for (int c = t.c_first; c <= t.c_last; c += 2) {
+          const float4* p0 = part(c);
+          const float4* p1 = part(min(c + 1, t.c_last));
+          const float4 a0 = __ldcg(p0), a1 = __ldcg(p0 + 128), b0 = __ldcg(p1), b1 = __ldcg(p1 + 128);
+          add(a0, a1);
+          if (c < t.c_last) add(b0, b1);
         }
       }
-      emit<NMAT, PAIR>(p, a, cc, t.mt, t.slot0, t.nvalid, r, bias, turn);
+      emit<NMAT, PAIR>(p, a, cc, t.mt, t.slot0, t.nvalid, r, bias, res, turn);
     }
   }
 }
@@ -1145,24 +1182,65 @@ struct GLayout {
   size_t smem = 0;
 };
 
-// Columns per tile, at most: twice an average group's rows, since a group that
-// needs two column tiles has its weights rebuilt twice (they come from L2 the
-// second time), and at least 32, which costs little; one group takes what it
-// needs.  A wider tile than needed takes shared memory from the weight ring.
-// Measured with 8 experts of 14336 x 4096, SwiGLU: 8 rows on average 231 us at
-// 16 columns, 217 at 32; 64 rows 421 at 64, 267 at 128, 289 at 192.
-int pick_cap(int n_rows, int E, int nmat) {
-  const int64_t most = nmat == 2 ? 192 : 256;
-  int64_t want = n_rows;
-  if (E > 1) want = std::min<int64_t>(n_rows, std::max<int64_t>(32, 2 * ((static_cast<int64_t>(n_rows) + E - 1) / E)));
-  const int64_t tiles = (want + most - 1) / most;
-  want = E > 1 ? std::min(want, most) : (want + tiles - 1) / tiles;
-  return static_cast<int>(std::max<int64_t>(16, (want + 15) / 16 * 16));
+// Columns per tile, at most: the width for which an estimate of the launch is
+// smallest, in units of one k-block of a tile (about 500 cycles).  Wide tiles
+// rebuild each weight tile less often, narrow ones give more tiles to spread
+// over the CTAs and less to carry through the epilogue.  A k-block costs the
+// larger of the rebuild (0.7) and the MMAs (2 cycles per column), the weights
+// once from HBM 1.06 (per column tile when tiles are shared out and the
+// weights outgrow L2: their column tiles then come at different times); a
+// tile's epilogue 0.7 per 8 columns and 2, behind the next tile's k-blocks
+// where there are two accumulators; sharing a tile out the writing (half of
+// that), a ticket and the adding up of the parts, which 6 groups of warps do 8
+// columns each at a time.  A wider tile has to win by 3%: it takes shared
+// memory from the weight ring.  Measured against the widest
+// tile: 512 rows of 1024 x 1024 8.0 us at 64 columns, 15.2 at 256; 128 rows of
+// 1024 x 4096 11.8 at 32, 23.3 at 128; 450 rows of 5896 x 1088 15.6 at 160,
+// 17.9 at 240; but 1000 rows of 4096 x 4096 38.5 at 256, 51.5 at 176.
+// Groups of several experts vary in size: an average group of `avg` rows is
+// taken to need one column tile of 2 avg columns, else avg / width + 3/4, and
+// no width below 32 is taken (8 experts of 14336 x 4096, SwiGLU: 8 rows on
+// average 231 us at 16, 217 at 32; 64 rows 377 at 96, 267 at 128, 289 at 192).
+int pick_cap(int n_rows, int E, int nmat, int n_mt, int KB, int sms) {
+  static const int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};
+  const int most = std::min(nmat == 2 ? 192 : 256, (n_rows + 15) / 16 * 16);
+  const double groups = std::min(n_rows, E), avg = n_rows / groups;
+  const double weights = nmat * groups * n_mt * KB;  // tiles of them
+  int best = most;
+  double least = 0;
+  for (const int width : kWidths) {
+    int cap = std::min(width, most);
+    double cols = cap >= 2 * avg ? 1.0 : avg / cap + 0.75;
+    if (E == 1) {
+      const int n_nt = (n_rows + cap - 1) / cap;
+      cap = ((n_rows + n_nt - 1) / n_nt + 15) / 16 * 16;
+      cols = n_nt;
+    } else if (cap < std::min(32, most)) {
+      continue;
+    }
+    const double tiles = groups * n_mt * cols, chunks = std::max(1.0, avg / cols / 8), waves = std::ceil(tiles / sms);
+    const double main = KB * nmat * std::max(0.7, std::min<double>(cap, avg / cols + 15) * 0.004);
+    const double epi = 0.7 * chunks * nmat + 2;
+    const bool two = 2 * nmat * cap <= 256;
+    const double each = two ? std::max(main, epi) : main + epi;
+    const double hbm = 1.06 * weights / sms;
+    const double whole = std::max(hbm, waves * each + (two ? std::min(main, epi) : 0.0));
+    const double again = weights * 12304 > 64e6 ? cols : 1.0;
+    const double shared = std::max(hbm * again, tiles / sms * each) + 0.5 * epi + 4 +
+                          nmat * std::ceil(chunks / 6) * (1 + 0.35 * std::max(2.0, sms / tiles));
+    const double cost = std::min(whole, shared);
+    if (least == 0 || cost < 0.97 * least) {
+      least = cost;
+      best = cap;
+    }
+    if (width >= most) break;
+  }
+  return best;
 }
 
-bool make_glayout(int n_rows, int E, int nmat, GLayout* out) {
+bool make_glayout(int cap, int E, int nmat, GLayout* out) {
   GLayout l;
-  l.cap = pick_cap(n_rows, E, nmat);
+  l.cap = cap;
   // tensor memory: accumulators (n_acc buffers x n_iss issuers x cap
   // columns), then 32 columns per A tile
   l.n_acc = 2 * nmat * l.cap <= 256 ? 2 : 1;
@@ -1220,13 +1298,16 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   // Measured, pairs against single tiles: 8 x 512 rows of 4096 x 14336 644 /
   // 778 us, 8 x 64 rows 140 / 180; but 512 rows of one 14336 x 4096 matrix
   // (73 pair units per CTA) 87 / 76.
-  const int cap1 = pick_cap(std::max(n_rows, 1), E, 1), cap2 = pick_cap(std::max(n_rows, 1), E, 2);
+  const int n = std::max(n_rows, 1);
+  int cap = swiglu ? 0 : pick_cap(n, E, 1, g.n_mt, g.KB, sms);
+  const int cap2 = pick_cap(n, E, 2, swiglu ? g.n_mt : (g.n_mt + 1) / 2, g.KB, sms);
   const int64_t pair_units =
       static_cast<int64_t>((g.n_mt + 1) / 2) * std::max<int64_t>(E > 1 ? std::min(n_rows, E) : 1, n_rows / cap2) * g.KB;
-  g.pair = !swiglu && g.n_mt > 1 && cap1 > kPairCap && pair_units >= kPairUnits * sms;
+  g.pair = !swiglu && g.n_mt > 1 && cap > kPairCap && pair_units >= static_cast<int64_t>(kPairUnits) * sms;
   const int nmat = swiglu || g.pair ? 2 : 1;
+  if (nmat == 2) cap = cap2;
   if (g.pair) g.n_mt = (g.n_mt + 1) / 2;
-  if (!make_glayout(std::max(n_rows, 1), E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
+  if (!make_glayout(cap, E, nmat, &g.lay)) return UW_ERR_UNSUPPORTED_SHAPE;
   // the most units any split of n_rows into E groups can give
   const int64_t tiles = std::min<int64_t>(n_rows, n_rows / g.lay.cap + E);
   const int64_t units = tiles * g.n_mt * g.KB;
@@ -1400,7 +1481,7 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   // Measured by switching it off (0) and to 1000: 256 rows of 14336 x 4096
   // 44.9 us split, 37.1 whole (64 k-blocks against 48); 64 experts of
   // 2048 x 1024 37.4 / 35.7; but one row of 4096 x 14336 20.5 / 57.6
-  p.join = 4 + g.lay.cap / 8;
+  p.join = 4 + g.lay.cap / 16;
   // (the permuting kernel lets this one in after waiting for its own
   // predecessor, which may have written the offsets)
   p.early = a.offsets == nullptr || a.offsets_ready || g.permuted;

@@ -573,7 +573,7 @@ UW_API size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, in
  * y: device [n_rows, rows], BF16 or FP32 (epi->out_type); epi may be NULL
  * (plain BF16 product).  Slots outside [offsets[0], offsets[n_experts]) are
  * left as they were.  The matrix of an expert without slots is not read.
- * n_rows = 0 launches nothing.
+ * n_rows = 0 launches nothing.  y overlaps neither x nor rows nor offsets.
  * Sums are FP32; their order depends only on the shapes, n_rows, the offsets
  * and the SM count.  cols <= 32768.
  * The table and the matrices are constant (see the conventions above);

@@ -156,3 +156,252 @@ def test_epilogue_against_float64(batch, shape):
     uw.gemm_epilogue(dm, to_dev(x), r, ws, bias=to_dev(bias[0]), activation="silu", residual=r)
     ws.check()
     assert np.array_equal(to_host_u16(r), to_host_u16(y))
+
+
+# ---------------------- schedules of larger products -------------------------
+# Waves of whole tiles, shared tiles, column tiles, row-tile pairs, permuted
+# and gathered rows.  The float64 reference runs on the GPU (torch.double).
+
+def f64(bits):
+    import torch
+    return to_dev(bits).view(torch.bfloat16).double()
+
+
+def device_experts(mats):
+    ws = uw.Workspace(256)
+    return uw.Experts([uw.DeviceMatrix.encode_on_device(to_dev(m)).prepare_direct_palette(ws, keep_idx4=False) for m in mats])
+
+
+def worst_excess(y, mats, x, rows, offsets, K, swiglu_with=None):
+    """max(|y - ref| - bound) over all slots (bounds of moe_util, on the GPU)."""
+    import torch
+    worst = -np.inf
+    xd = f64(x)
+    for e, w in enumerate(mats):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b <= a:
+            continue
+        xe = xd[torch.from_numpy(rows[a:b].astype(np.int64)).cuda()]
+        wd = f64(w)
+        v, d = xe @ wd.T, K * 2.0 ** -23 * (xe.abs() @ wd.abs().T)
+        if swiglu_with is not None:
+            ud = f64(swiglu_with[e])
+            u, du = xe @ ud.T, K * 2.0 ** -23 * (xe.abs() @ ud.abs().T)
+            s = v / (1 + torch.exp(-v))
+            d = 1.1 * d * u.abs() + s.abs() * du + 1.1 * d * du + 16 * 2.0 ** -24 * (v.abs() + s.abs()) * u.abs()
+            v = s * u
+        if y.dtype != torch.float32:
+            d = d + 2.0 ** -8 * (v.abs() + d)
+        worst = max(worst, float(((y[a:b].double() - v).abs() - d).max()) - 1e-30)
+    return worst
+
+
+BIG = [  # rows, cols, group sizes
+    (4096, 1024, [50, 200, 0, 131, 64, 7, 90, 33]),   # waves and shared tiles
+    (14336, 512, [500, 33]),                          # column tiles, waves
+    (2048, 1024, [3] * 64),                           # many small groups
+    (1096, 8192, [2900, 2860]),                       # row-tile pairs, the last one half empty
+    (4096, 4096, [40, 0, 21]),                        # fewer tiles than CTAs, left whole
+    (512, 4096, [1, 2]),                              # and shared out
+]
+
+
+@pytest.mark.parametrize("case", range(len(BIG)))
+@pytest.mark.parametrize("scattered", [False, True])
+def test_larger_products_against_float64(case, scattered):
+    import torch
+    rows, cols, counts = BIG[case]
+    mats = expert_weights(len(counts), rows, cols, 800 + 100 * case, rate=1e-4)
+    off = offsets_of(counts)
+    n = int(off[-1])
+    x = synth.activations(n // 2 + 1 if scattered else n, cols, 801)
+    r = random_rows(off, x.shape[0], n, 802) if scattered else np.arange(n)
+    ex = device_experts(mats)
+    y = torch.empty(n, rows, dtype=torch.bfloat16, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, n))
+    xd, rd, offd = to_dev(x), to_dev(r.astype(np.int32)) if scattered else None, to_dev(off)
+    uw.gemm_grouped(ex, xd, offd, y, ws, rows=rd)
+    ws.check()
+    assert worst_excess(y, mats, x, r, off, cols) <= 0
+    again = torch.empty_like(y)
+    uw.gemm_grouped(ex, xd, offd, again, ws, rows=rd)
+    ws.check()
+    assert torch.equal(y, again)  # the sums do not depend on timing
+    z = torch.empty(n, rows, dtype=torch.float32, device="cuda")
+    uw.gemm_grouped(ex, xd, offd, z, ws, rows=rd)
+    ws.check()
+    assert worst_excess(z, mats, x, r, off, cols) <= 0
+    assert torch.equal(z.to(torch.bfloat16), y)
+
+
+@pytest.mark.parametrize("rows,cols,counts", [(4096, 1024, [50, 200, 0, 131]), (14336, 512, [500, 33]), (1000, 2048, [9, 30, 1])])
+def test_larger_swiglu_against_float64(rows, cols, counts):
+    import torch
+    gs, us = expert_weights(len(counts), rows, cols, 900), expert_weights(len(counts), rows, cols, 920)
+    off = offsets_of(counts)
+    n = int(off[-1])
+    x = synth.activations(n // 2 + 1, cols, 901)
+    r = random_rows(off, x.shape[0], n, 902)
+    eg, eu = device_experts(gs), device_experts(us)
+    h = torch.empty(n, rows, dtype=torch.bfloat16, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(eg, n, swiglu=True))
+    uw.gemm_grouped_swiglu(eg, eu, to_dev(x), to_dev(off), h, ws, rows=to_dev(r))
+    ws.check()
+    assert worst_excess(h, gs, x, r, off, cols, swiglu_with=us) <= 0
+
+
+def test_six_hundred_experts():
+    mats = expert_weights(6, 128, 64, 930)
+    dms = [device_matrix(m) for m in mats]
+    E = 600
+    ex = uw.Experts([dms[e % 6] for e in range(E)])  # the same matrix many times
+    counts = [(e * 7) % 4 for e in range(E)]
+    off = offsets_of(counts)
+    n = int(off[-1])
+    x = synth.activations(n, 64, 931)
+    got = run_grouped(ex, x, off, n)
+    ok, worst = check_slots(got, grouped_ref([mats[e % 6] for e in range(E)], x, np.arange(n), off))
+    assert ok, worst
+
+
+def test_more_than_two_to_the_31_output_values():
+    import torch
+    rows, cols, batch = 32768, 64, 66000
+    w = synth.weight_matrix(rows, cols, 0.02, 1e-3, 200.0, 940)
+    dm = uw.DeviceMatrix.encode_on_device(to_dev(w)).prepare_direct_palette(uw.Workspace(256), keep_idx4=False)
+    x = synth.activations(batch, cols, 941)
+    y = torch.empty(batch, rows, dtype=torch.bfloat16, device="cuda")
+    ws = uw.Workspace(uw.epilogue_workspace_bytes(dm, batch))
+    uw.gemm_epilogue(dm, to_dev(x), y, ws)
+    ws.check()
+    for a in (0, 32760, 65536, batch - 40):
+        part = y[a:a + 40]
+        assert worst_excess(part, [w], x[a:a + 40], np.arange(40), [0, 40], cols) <= 0
+    del y
+
+
+# ------------------------------ special values -------------------------------
+
+def test_nan_and_infinite_activations_stay_in_their_slot():
+    mats = expert_weights(2, 256, 256, 950)
+    off = offsets_of([20, 13])
+    x = synth.activations(33, 256, 951)
+    clean = run_grouped(experts_of(mats), x, off, 33)
+    x[4, 7] = 0x7FC0    # NaN
+    x[25, 100] = 0x7F80  # +inf
+    got = run_grouped(experts_of(mats), x, off, 33)
+    keep = np.ones(33, bool)
+    keep[[4, 25]] = False
+    assert np.array_equal(got[keep], clean[keep])
+    assert np.isnan(got[4]).all() and not np.isfinite(got[25]).any()
+
+
+def test_weights_of_every_bf16_pattern():
+    """Infinities, NaNs, zeros and subnormals among the weights: y is what the
+    IEEE sum gives, row by row."""
+    w = synth.all_patterns_matrix()  # 1024 x 64
+    finite = np.isfinite(O.bf16_to_f64(w)).all(axis=1)
+    dm = device_matrix(w)
+    x = synth.f32_to_bf16_bits(np.eye(64, dtype=np.float32)[:8])  # picks out columns
+    import torch
+    y = torch.empty(8, 1024, dtype=torch.float32, device="cuda")
+    ws = uw.Workspace(uw.epilogue_workspace_bytes(dm, 8))
+    uw.gemm_epilogue(dm, to_dev(x), y, ws)
+    ws.check()
+    got = y.cpu().numpy().T.astype(np.float64)
+    assert np.array_equal(got[finite], O.bf16_to_f64(w)[finite][:, :8])
+    assert np.isnan(got[~finite]).any(axis=1).all()  # 0 * inf or a NaN in the row
+
+
+# --------------------------- streams and workspaces --------------------------
+
+def test_two_streams_with_their_own_workspaces():
+    import torch
+    mats = expert_weights(4, 1024, 2048, 960)
+    ex = experts_of(mats)
+    off = to_dev(offsets_of([5, 40, 0, 19]))
+    xs = [to_dev(synth.activations(64, 2048, 961 + i)) for i in range(2)]
+    want = []
+    for x in xs:
+        y, ws = empty_bf16(64, 1024), uw.Workspace(uw.grouped_workspace_bytes(ex, 64))
+        uw.gemm_grouped(ex, x, off, y, ws, activation="silu")
+        ws.check()
+        want.append(y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    wss = [uw.Workspace(uw.grouped_workspace_bytes(ex, 64)) for _ in xs]
+    outs = [empty_bf16(64, 1024) for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, x, y, ws in zip(streams, xs, outs, wss):
+            uw.gemm_grouped(ex, x, off, y, ws, activation="silu", stream=s)
+    torch.cuda.synchronize()
+    for y, w, ws in zip(outs, want, wss):
+        ws.check()
+        assert torch.equal(y, w)
+
+
+def test_one_workspace_for_calls_of_many_sizes():
+    """The regions start at the same offsets for every call: products of
+    different shapes, and the dense GEMM, take turns on one workspace."""
+    import torch
+    mats = expert_weights(3, 1024, 2048, 970)
+    ex = experts_of(mats)
+    dm = ex.matrices[0]
+    ws = uw.Workspace(max(uw.grouped_workspace_bytes(ex, 300, swiglu=True), uw.workspace_bytes(dm, uw.PIPE_DIRECT, 100)))
+    results = {}
+    for turn in range(3):
+        for n in (1, 300, 7, 64, 150):
+            off = to_dev(offsets_of([n // 3, 0, n - n // 3]))
+            x = to_dev(synth.activations(n, 2048, 971))
+            y, h, g = empty_bf16(n, 1024), empty_bf16(n, 1024), empty_bf16(min(n, 100), 1024)
+            uw.gemm_grouped(ex, x, off, y, ws)
+            uw.gemm_grouped_swiglu(ex, ex, x, off, h, ws)
+            uw.gemm_direct_palette(dm, x[:100], g, ws)
+            ws.check()
+            out = [to_host_u16(t) for t in (y, h, g)]
+            if turn == 0:
+                results[n] = out
+            else:
+                assert all(np.array_equal(a, b) for a, b in zip(out, results[n])), n
+
+
+# --------------------------------- refusals ----------------------------------
+
+def test_refusals_launch_nothing():
+    import torch
+    ex = experts_of(expert_weights(2, 128, 128, 980))
+    other = experts_of(expert_weights(2, 256, 128, 982))
+    x, y = empty_bf16(6, 128), empty_bf16(6, 128)
+    off = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, 6, swiglu=True))
+    small = uw.Workspace(1024)
+    dm = ex.matrices[0]
+    bad = [
+        lambda: uw.gemm_grouped(ex, x[:, :64], off, y, ws),                       # columns
+        lambda: uw.gemm_grouped(ex, empty_bf16(128, 6).t(), off, y, ws),          # not contiguous
+        lambda: uw.gemm_grouped(ex, x.float(), off, y, ws),                       # type
+        lambda: uw.gemm_grouped(ex, x.cpu(), off, y, ws),                         # device
+        lambda: uw.gemm_grouped(ex, x, off.long(), y, ws),
+        lambda: uw.gemm_grouped(ex, x, off[:2], y, ws),
+        lambda: uw.gemm_grouped(ex, x, off, y.double(), ws),
+        lambda: uw.gemm_grouped(ex, x[:5].contiguous(), off, y, ws),              # fewer rows of x than slots
+        lambda: uw.gemm_grouped(ex, x, off, y, ws, rows=off),
+        lambda: uw.gemm_grouped(ex, x, off, y, ws, bias=empty_bf16(128)),
+        lambda: uw.gemm_grouped(ex, x, off, y, ws, residual=empty_bf16(6, 64)),
+        lambda: uw.gemm_grouped(ex, x, off, y, ws, activation="swish"),
+        lambda: uw.gemm_grouped(ex, x, off, y, small),
+        lambda: uw.gemm_grouped_swiglu(ex, other, x, off, y, ws),
+        lambda: uw.gemm_grouped_swiglu(ex, ex, x, off, empty_bf16(6, 64), ws),
+        lambda: uw.gemm_epilogue(dm, x, y, small),
+        lambda: uw.gemm_epilogue(dm, x, empty_bf16(5, 128), ws),
+        lambda: uw.gemm_epilogue(dm, x, y, ws, bias=empty_bf16(1, 128)),
+        lambda: uw.Experts([dm, other.matrices[0]]),
+        lambda: uw.Experts([uw.DeviceMatrix(uw.encode(synth.weight_matrix(128, 128, 0.02, 0.0, 1.0, 1)))]),  # no pack
+    ]
+    n = uw.launch_count()
+    for i, call in enumerate(bad):
+        with pytest.raises(uw.UwError):
+            call()
+            pytest.fail(f"refusal {i}")
+    assert uw.launch_count() == n

@@ -32,10 +32,11 @@
 //    through the same rings and share the activation tile; both sums stay in
 //    tensor memory and meet in the epilogue, so g and u are never rounded or
 //    stored.
-//  * The rows of x arrive in TMA boxes of 64 and 16 rows, or, where a group's rows are
-//    scattered, by TMA gather (4 row numbers per copy) while groups are small;
-//    the gather takes about 75 cycles per 4 rows, so beyond kGatherCap rows
-//    per tile a small kernel first copies the rows next to each other.
+//  * The rows of x arrive in TMA boxes of 64 and 16 rows, or, where a group's
+//    rows are scattered, by TMA gather (4 row numbers per copy) while groups
+//    are small; the gather takes about 75 cycles per 4 rows, so beyond
+//    kGatherCap rows per tile a small kernel first copies the rows next to
+//    each other.
 //  * A tile shared by several CTAs: each writes its FP32 sums to a slot of
 //    its own (a CTA has at most two such tiles, its first and its last) and
 //    takes a ticket; the last adds all of them in CTA order and runs the
@@ -90,7 +91,7 @@ struct GParams {
   int vcap;             // verbatim rows staged per record
   int join;             // what joining a shared tile costs, in k-blocks
   int early;            // offsets are not the previous kernel's output
-  int gather;           // x rows by number (TMA gather), else 16-row boxes
+  int gather;           // x rows by number (TMA gather), else in boxes
   const int32_t* offsets;
   const int32_t* rows;
   const ExpertDesc* table[2];
@@ -115,9 +116,9 @@ struct Todo {
 // each other, are dealt out in waves of one tile per CTA: CTAs that work at
 // the same time share weight tiles (the column tiles of a row tile) and
 // activation tiles through L2.  What does not fill waves evenly (up to two
-// tiles per CTA) is cut into equal runs of k-blocks (stream-K).  Contiguous shares for all tiles
-// instead read the weights of three column tiles three times from HBM: the
-// first CTA's second column tile came when L2 had long moved on.
+// tiles per CTA) is cut into equal runs of k-blocks (stream-K).  Contiguous
+// shares for all tiles instead read the weights of three column tiles three
+// times from HBM: a CTA came to its next column tile when L2 had moved on.
 struct Share {
   int grid, waves;        // CTAs that take part, whole tiles per CTA
   int sk_each, sk_long;   // k-blocks of the tiles after the waves: lengths of the runs
@@ -220,7 +221,8 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
 // chain of divisions, and the exact one takes 40 instructions.
 __device__ __forceinline__ int quick_div(int a, int b) {
   int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
-  int r = a - q * b;
+  // (modulo 2^32: q b may pass 2^31 where a is near it)
+  int r = static_cast<int>(static_cast<uint32_t>(a) - static_cast<uint32_t>(q) * static_cast<uint32_t>(b));
   while (r < 0) {
     --q;
     r += b;
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.gather) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            r[q] = __ldg(p.rows + s.slot0 + min(4 * lane + q, s.nvalid - 1));
+            r[q] = __ldcg(p.rows + s.slot0 + min(4 * lane + q, s.nvalid - 1));
             if (r[q] < 0 || r[q] >= p.x_rows) {
               record_status(p.status, UW_ERR_INVALID_ARG);
               r[q] = 0;
@@ -1162,7 +1164,7 @@ __global__ void __launch_bounds__(256) permute_kernel(const PermuteParams p) {
     const uint4* src = p.x + static_cast<int64_t>(r) * p.pieces;
     uint4* dst = p.out + static_cast<int64_t>(s) * p.pieces;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < p.pieces; i += 256) dst[i] = __ldg(src + i);
+    for (int i = threadIdx.x; i < p.pieces; i += 256) dst[i] = __ldcg(src + i);
   }
 }
 

@@ -420,10 +420,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
     bool have[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int s = j0 + q < p.k ? __ldg(slots + j0 + q) : -1;
+      const int s = j0 + q < p.k ? slots[j0 + q] : -1;
       have[q] = s >= 0 && s < p.n_rows;
       if (have[q]) {
-        w[q] = __ldg(weights + j0 + q);
+        w[q] = weights[j0 + q];
         load_part<VEC, FP32>(p.parts, static_cast<int64_t>(s) * p.cols + c, v[q]);
       }
     }

@@ -84,6 +84,13 @@ def test_slots_outside_the_groups_stay_as_they_were():
     assert ok, worst
 
 
+def test_no_group_has_a_slot():
+    mats = expert_weights(2, 256, 256, 535)
+    x = synth.activations(9, 256, 536)
+    got = run_grouped(experts_of(mats), x, np.array([3, 3, 3], np.int32), 9)
+    assert len(set(got.ravel())) == 1  # all as they were
+
+
 @pytest.mark.parametrize("act", sorted(uw.ACTIVATIONS))
 @pytest.mark.parametrize("fp32", [False, True])
 def test_grouped_epilogue(act, fp32):
@@ -135,7 +142,7 @@ def test_many_verbatim_rows_and_mixed_palettes(rate):
     assert ok, worst
 
 
-@pytest.mark.parametrize("batch", [1, 16, 17, 100, 256, 257, 600])
+@pytest.mark.parametrize("batch", [1, 16, 17, 49, 63, 65, 100, 256, 257, 600])
 @pytest.mark.parametrize("shape", [(256, 512), (1000, 4096)])
 def test_epilogue_against_float64(batch, shape):
     rows, cols = shape

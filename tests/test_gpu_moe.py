@@ -44,7 +44,7 @@ def check_route(r, logits, k, renormalize=True):
 
 
 @pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 129, 700])
-@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (8, 2), (33, 5), (64, 8), (130, 3), (256, 8), (1000, 32)])
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (8, 2), (33, 5), (64, 8), (130, 3), (256, 8), (40, 32), (200, 31), (1000, 32)])
 def test_route_against_float64(T, E, k):
     logits = np.random.default_rng(T * 1000 + E).standard_normal((T, E)).astype(np.float32) * 2
     for ren in (True, False):
@@ -231,6 +231,20 @@ def test_block_against_float64(sparse_mlp, T, k):
         ref, bound = block_ref(gs, us, ds, x, logits, k, r, ren)
         got = bf16_f64(to_host_u16(y))
         assert np.all(np.abs(got - ref) <= bound), float(np.max(np.abs(got - ref) - bound))
+
+
+def test_block_of_padded_tokens_only(sparse_mlp):
+    import torch
+    _, ex = sparse_mlp
+    T, k, d = 20, 2, ex[2].rows
+    x, res = to_dev(synth.activations(T, d, 665)), to_dev(synth.activations(T, d, 666))
+    logits = torch.full((T, len(ex[0])), -math.inf, device="cuda")
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    y, z = empty_bf16(T, d), empty_bf16(T, d)
+    uw.moe_block(*ex, x, logits, k, y, ws, residual=res)
+    uw.moe_block(*ex, x, logits, k, z, ws)
+    ws.check()
+    assert torch.equal(y, res) and not bool(z.any())
 
 
 def test_block_equals_its_four_calls(sparse_mlp):

@@ -66,6 +66,10 @@ constexpr int kWarpW = 0, kWarpX = 1, kWarpMma = 2, kWarpRebuild = 4, kWarpEpi =
 constexpr int kThreads = 32 * (kWarpEpi + 4);
 constexpr int kMaxSlots = 16;
 constexpr int kWBatch = 4;  // tiles that the weight producer issues at a time
+// Columns (times matrices) of a CTA's last tile above which all warps empty its
+// accumulators: 1000 rows of 4096 x 4096 34.1 us against 38.5, 664 rows of 7292
+// x 576 with GELU 32.3 / 37.6; one row of 4096 x 4096 takes 1 us more by it.
+constexpr int kTogether = 48;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBody = 12304, kBodyIdx = 8192, kBodyMask = 12288;  // pack record of a tile (uw.h)
 constexpr uint32_t kMinTail = 8;  // verbatim rows staged per tile, at least
@@ -142,8 +146,10 @@ struct GBars {
   uint64_t acc_full[2], acc_empty[2], drain[kMaxIssuers];
   uint32_t tail_first[kMaxSlots];  // per weight slot: first verbatim row of its tile
   uint32_t tmem_base, abort, n_todo;
+  // the last segment, when all warps finish it: accumulator buffer, first tile
+  uint32_t together, last_acc, last_tile;
   Share share;
-  Seg first;
+  Seg first, last;     // segments
   ExpertDesc desc[2];  // the first segment's matrices
   Todo todo[2];
 };
@@ -320,6 +326,10 @@ __device__ __forceinline__ void seg_init(Seg& s, const SchedEntry* sched, const 
   s.e = 0;
   s.tile_u = 0;
   seg_here(s, sched, p, h, cta);
+}
+// whether the segment is the share's last
+__device__ __forceinline__ bool seg_last(const Seg& s, const Share& h) {
+  return s.wave < h.waves ? s.wave + 1 == h.waves && h.u0 >= h.u1 : s.u + (s.kb1 - s.kb0) >= h.u1;
 }
 // false when the share is done
 __device__ __forceinline__ bool seg_next(Seg& s, const SchedEntry* sched, const GParams& p, const Share& h, int cta) {
@@ -566,6 +576,86 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
                : "memory");
 }
 
+// Whether the segment is part of a tile that other CTAs work on too.
+__device__ __forceinline__ bool is_part(const Seg& s, const GParams& p) { return s.kb1 - s.kb0 != p.KB; }
+
+// A segment's sums out of tensor memory: to y, or, when it is a part of a
+// tile, to the CTA's partial slot.  Warps 4 k .. 4 k + 3 take every n_groups-th
+// 8 columns from `group` on; row r of the tile is the thread's.
+template <int NMAT, bool PAIR>
+__device__ __forceinline__ void drain(const GParams& p, const Share& share, const Seg& s, int cta, uint32_t taddr,
+                                      int first_tile, int r, int group, int n_groups, float* turn) {
+  const int n_kb = s.kb1 - s.kb0;
+  const int n_chunks = (s.nvalid + 7) >> 3;
+  auto sums = [&](int cc, float (&a)[NMAT][8]) {
+    // With one matrix and two issuers: the issuers' sums in the order of their
+    // first k-block (a segment of one k-block has only one)
+    uint32_t v[2][8];
+    const uint32_t at = taddr + static_cast<uint32_t>(cc * 8);
+    if constexpr (NMAT == 2) {
+      tmem_ld8(at, v[0]);
+      tmem_ld8(at + p.cap, v[1]);
+    } else {
+      const uint32_t i0 = static_cast<uint32_t>(first_tile % p.n_iss);
+      tmem_ld8(at + i0 * p.cap, v[0]);
+      if (p.n_iss == 2 && n_kb > 1) tmem_ld8(at + (i0 ^ 1u) * p.cap, v[1]);
+    }
+    tc_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[0][j] = __uint_as_float(v[0][j]);
+      if constexpr (NMAT == 2) a[NMAT - 1][j] = __uint_as_float(v[1][j]);
+      else if (p.n_iss == 2 && n_kb > 1) a[0][j] += __uint_as_float(v[1][j]);
+    }
+  };
+  if (n_kb == p.KB) {
+    float bias[NMAT];
+    load_bias<NMAT, PAIR>(p, s.e, s.mt, r, bias);
+#pragma unroll 1
+    for (int cc = group; cc < n_chunks; cc += n_groups) {
+      float a[NMAT][8];
+      uint4 res[NMAT];
+      load_residual<NMAT, PAIR>(p, cc, s.mt, s.slot0, s.nvalid, r, res);
+      sums(cc, a);
+      emit<NMAT, PAIR>(p, a, cc, s.mt, s.slot0, s.nvalid, r, bias, res, turn);
+    }
+    return;
+  }
+  // the CTA's slot 0 holds the tile that opens its run, slot 1 a later one;
+  // [matrix][chunk of 8 columns][half][weight row][4 columns]
+  float4* mine = reinterpret_cast<float4*>(
+      p.partials + (2 * static_cast<int64_t>(cta) + (share.u0 >= s.tile_u ? 0 : 1)) * p.partial_stride);
+#pragma unroll 1
+  for (int cc = group; cc < n_chunks; cc += n_groups) {
+    float a[NMAT][8];
+    sums(cc, a);
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      float4* dst = mine + (m * n_chunks + cc) * 256 + r;
+      __stcg(dst, make_float4(a[m][0], a[m][1], a[m][2], a[m][3]));
+      __stcg(dst + 128, make_float4(a[m][4], a[m][5], a[m][6], a[m][7]));
+    }
+  }
+}
+
+// One thread, after every store of the part has met it at a barrier: takes the
+// tile's ticket, and notes the tile when this was the last part.
+__device__ __forceinline__ void deliver(const GParams& p, const Share& share, const Seg& s, GBars* bars) {
+  const int c_first = unit_owner(s.tile_u, share);
+  const int c_last = unit_owner(s.tile_u + p.KB - 1, share);
+  // a CTA opens at most one tile that others finish: its counter
+  if (ticket(p.counters + c_first) != static_cast<uint32_t>(c_last - c_first)) return;
+  p.counters[c_first] = 0;  // all have arrived: ready for the next launch
+  Todo& t = bars->todo[bars->n_todo++];
+  t.e = s.e;
+  t.mt = s.mt;
+  t.slot0 = s.slot0;
+  t.nvalid = s.nvalid;
+  t.c_first = c_first;
+  t.c_last = c_last;
+  t.first_slot = units_before(c_first, share) >= s.tile_u ? 0 : 1;
+}
+
 // ------------------------------- the kernel ----------------------------------
 template <int NMAT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -609,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bars->abort = 0;
       bars->n_todo = 0;
+      bars->together = 0;
     }
     mbar_fence_init();
     __syncwarp();
@@ -987,121 +1078,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (work) {
       const int w = warp & 3;  // TMEM lanes 32 w ..
       const int r = w * 32 + lane;
-      const bool elected = warp == kWarpEpi && lane == 0;
       Seg s = bars->first;
       uint32_t seg = 0;
       int first_tile = 0;  // the segment's first tile in the CTA's sequence
       float* turn = reinterpret_cast<float*>(smem + p.turn_off) + w * 256;
       do {
         const uint32_t ab = seg % p.n_acc;
+        if (seg_last(s, share) && !is_part(s, p) && (s.nvalid * NMAT > kTogether)) {
+          // left to all warps
+          if (warp == kWarpEpi && lane == 0) {
+            bars->last = s;
+            bars->last_acc = ab;
+            bars->last_tile = first_tile;
+            bars->together = 1;
+          }
+          break;
+        }
         bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bars->acc_full[ab], (seg / p.n_acc) & 1, &bars->abort, p.status));
         if (!group_and(ok)) break;
         tc_fence_after();
-        const int n_kb = s.kb1 - s.kb0;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap);
-        const int n_chunks = (s.nvalid + 7) >> 3;
-        // this CTA's sums of 8 columns, per matrix.  With one matrix and two
-        // issuers: the issuers' sums in the order of their first k-block (a
-        // segment of one k-block has only one)
-        auto own_sums = [&](int cc, float (&a)[NMAT][8]) {
-          uint32_t v[2][8];
-          const uint32_t at = taddr + static_cast<uint32_t>(cc * 8);
-          if constexpr (NMAT == 2) {
-            tmem_ld8(at, v[0]);
-            tmem_ld8(at + p.cap, v[1]);
-          } else {
-            const uint32_t i0 = static_cast<uint32_t>(first_tile % p.n_iss);
-            tmem_ld8(at + i0 * p.cap, v[0]);
-            if (p.n_iss == 2 && n_kb > 1) tmem_ld8(at + (i0 ^ 1u) * p.cap, v[1]);
-          }
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            a[0][j] = __uint_as_float(v[0][j]);
-            if constexpr (NMAT == 2) a[NMAT - 1][j] = __uint_as_float(v[1][j]);
-            else if (p.n_iss == 2 && n_kb > 1) a[0][j] += __uint_as_float(v[1][j]);
-          }
-        };
-        float bias[NMAT];
-        load_bias<NMAT, PAIR>(p, s.e, s.mt, r, bias);
-        if (n_kb == p.KB) {
-#pragma unroll 1
-          for (int cc = 0; cc < n_chunks; ++cc) {
-            float a[NMAT][8];
-            uint4 res[NMAT];
-            load_residual<NMAT, PAIR>(p, cc, s.mt, s.slot0, s.nvalid, r, res);
-            own_sums(cc, a);
-            emit<NMAT, PAIR>(p, a, cc, s.mt, s.slot0, s.nvalid, r, bias, res, turn);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
-        } else {
-          // part of a tile: contributors c_first..c_last
-          const int c_first = unit_owner(s.tile_u, share);
-          const int c_last = unit_owner(s.tile_u + p.KB - 1, share);
-          const int n_contrib = c_last - c_first + 1;
-          // contributor c's sums: its slot 0 when the tile opens its share,
-          // else slot 1; [matrix][chunk of 8 columns][half][weight row][4 columns]
-          auto part = [&](int c) -> float* {
-            const int which = units_before(c, share) >= s.tile_u ? 0 : 1;
-            return p.partials + (2 * static_cast<int64_t>(c) + which) * p.partial_stride;
-          };
-          float* mine = part(cta);
-#pragma unroll 1
-          for (int cc = 0; cc < n_chunks; ++cc) {
-            float a[NMAT][8];
-            own_sums(cc, a);
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m) {
-              float4* dst = reinterpret_cast<float4*>(mine) + (m * n_chunks + cc) * 256 + r;
-              __stcg(dst, make_float4(a[m][0], a[m][1], a[m][2], a[m][3]));
-              __stcg(dst + 128, make_float4(a[m][4], a[m][5], a[m][6], a[m][7]));
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
-          group_sync();  // every store of the group precedes the ticket
-          if (elected) {
-            // a CTA opens at most one tile that others finish: its counter
-            const bool last = ticket(p.counters + c_first) == static_cast<uint32_t>(n_contrib - 1);
-            if (last) p.counters[c_first] = 0;  // all have arrived: ready for the next launch
-            if (last) {
-              // every warp of the CTA adds the parts up once the roles are done
-              Todo& t = bars->todo[bars->n_todo++];
-              t.e = s.e;
-              t.mt = s.mt;
-              t.slot0 = s.slot0;
-              t.nvalid = s.nvalid;
-              t.c_first = c_first;
-              t.c_last = c_last;
-              t.first_slot = units_before(c_first, share) >= s.tile_u ? 0 : 1;
-            }
-          }
+        drain<NMAT, PAIR>(p, share, s, cta,
+                          tmem + (static_cast<uint32_t>(w * 32) << 16) + ab * p.n_iss * static_cast<uint32_t>(p.cap),
+                          first_tile, r, 0, 1, turn);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->acc_empty[ab]);
+        if (is_part(s, p)) {
+          group_sync();
+          if (warp == kWarpEpi && lane == 0) deliver(p, share, s, bars);
         }
         ++seg;
-        first_tile += n_kb * NMAT;
+        first_tile += (s.kb1 - s.kb0) * NMAT;
       } while (seg_next(s, sched, p, share, cta));
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  // Every role is done and every MMA has completed.  The rings are idle: their
+  // memory is where the warps turn values around from here on.
+  float* turn = reinterpret_cast<float*>(smem) + warp * 256;
+  const int r = (warp & 3) * 32 + lane;
+  if (bars->together) {
+    // ---- the last tile, whole and wide: all warps empty its accumulators (6
+    // groups of 4 warps, 8 columns each) instead of the epilogue's 4 with the
+    // others idle
+    tc_fence_after();
+    if (!*static_cast<volatile uint32_t*>(&bars->abort))
+      drain<NMAT, PAIR>(p, share, bars->last, cta,
+                        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                            bars->last_acc * p.n_iss * static_cast<uint32_t>(p.cap),
+                        static_cast<int>(bars->last_tile), r, warp >> 2, kThreads / 128, turn);
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
   // ---- tiles shared by several CTAs that this one completes (at most its
-  // first and its last): the contributors' parts, added in CTA order.  The
-  // rings are idle now; their memory is where the warps turn values around.
+  // first and its last): the contributors' parts, added in CTA order.
   for (int i = 0; i < static_cast<int>(bars->n_todo); ++i) {
     const Todo t = bars->todo[i];
-    const int r = (warp & 3) * 32 + lane;
     const int n_chunks = (t.nvalid + 7) >> 3;
     float bias[NMAT];
     load_bias<NMAT, PAIR>(p, t.e, t.mt, r, bias);
-    float* turn = reinterpret_cast<float*>(smem) + warp * 256;
 #pragma unroll 1
     for (int cc = warp >> 2; cc < n_chunks; cc += kThreads / 128) {
       float a[NMAT][8];
@@ -1192,7 +1233,8 @@ struct GLayout {
 // once from HBM 1.06 (per column tile when tiles are shared out and the
 // weights outgrow L2: their column tiles then come at different times); a
 // tile's epilogue 0.7 per 8 columns and 2, behind the next tile's k-blocks
-// where there are two accumulators; sharing a tile out the writing (half of
+// where there are two accumulators, a quarter of that for the last one of a
+// CTA; sharing a tile out the writing (half of
 // that), a ticket and the adding up of the parts, which 6 groups of warps do 8
 // columns each at a time.  A wider tile has to win by 3%: it takes shared
 // memory from the weight ring.  Measured against the widest
@@ -1226,7 +1268,8 @@ int pick_cap(int n_rows, int E, int nmat, int n_mt, int KB, int sms) {
     const bool two = 2 * nmat * cap <= 256;
     const double each = two ? std::max(main, epi) : main + epi;
     const double hbm = 1.06 * weights / sms;
-    const double whole = std::max(hbm, waves * each + (two ? std::min(main, epi) : 0.0));
+    const double last = std::min<double>(cap, avg / cols) * nmat > kTogether ? epi / 4 : epi;
+    const double whole = std::max(hbm, (waves - 1) * each + main + last);
     const double again = weights * 12304 > 64e6 ? cols : 1.0;
     const double shared = std::max(hbm * again, tiles / sms * each) + 0.5 * epi + 4 +
                           nmat * std::ceil(chunks / 6) * (1 + 0.35 * std::max(2.0, sms / tiles));
@@ -1483,7 +1526,7 @@ uw_status launch_grouped(const GroupedArgs& a, cudaStream_t s) {
   // Measured by switching it off (0) and to 1000: 256 rows of 14336 x 4096
   // 44.9 us split, 37.1 whole (64 k-blocks against 48); 64 experts of
   // 2048 x 1024 37.4 / 35.7; but one row of 4096 x 14336 20.5 / 57.6
-  p.join = 4 + g.lay.cap / 16;
+  p.join = 6 + g.lay.cap / 8;
   // (the permuting kernel lets this one in after waiting for its own
   // predecessor, which may have written the offsets)
   p.early = a.offsets == nullptr || a.offsets_ready || g.permuted;

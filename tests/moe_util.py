@@ -43,8 +43,11 @@ def epilogue_bound(v, dv, bias, act, residual, bf16):
     the activation's value or to v: 16 of 2^-24 (|v| + |act|); GELU's tanh
     form takes exp of a polynomial in v, off by 2^-22 |t| relative, and |t|
     times the result is at most 12 where the result is not negligible or
-    saturated: another 48 of 2^-24 (|v| + |act|) covers it.  BF16 adds one
-    rounding of the result."""
+    saturated: another 48 of 2^-24 (|v| + |act|) covers it.  GELU's normal
+    tail comes from a fit within 4.3e-8 and exp(-v^2 / 2) with the exponent
+    rounded, off by 2^-23 v^2 / 2 relative, and v^2 / 2 times the tail is at
+    most 0.2: less than the tanh form's.  BF16 adds one rounding of the
+    result."""
     s = v + bias
     dv = dv + F32 * np.abs(s)
     a = act_f64(s, act)

@@ -9,7 +9,7 @@ from mlp_huffman_coded_b200 import uw
 from oracle import uw_oracle as O
 
 from gpu_util import bf16_f64, device_matrix, empty_bf16, to_dev, to_host_u16
-from moe_util import check_slots, expert_weights, grouped_ref, swiglu_ref
+from moe_util import check_slots, epilogue_bound, expert_weights, grouped_ref, swiglu_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -318,6 +318,22 @@ def test_weights_of_every_bf16_pattern():
     got = y.cpu().numpy().T.astype(np.float64)
     assert np.array_equal(got[finite], O.bf16_to_f64(w)[finite][:, :8])
     assert np.isnan(got[~finite]).any(axis=1).all()  # 0 * inf or a NaN in the row
+
+
+@pytest.mark.parametrize("act", sorted(uw.ACTIVATIONS))
+def test_activations_over_their_range(act):
+    """W = identity: y = act(x) for every BF16 x of up to 2^7, both signs."""
+    import torch
+    bits = np.arange(0x4300, dtype=np.uint16)  # 0 .. 128
+    x = np.concatenate([bits, bits | 0x8000])
+    x = np.resize(x, -(-x.size // 64) * 64).reshape(-1, 64)
+    dm = device_matrix(synth.f32_to_bf16_bits(np.eye(64, dtype=np.float32)))
+    y = torch.empty(x.shape[0], 64, dtype=torch.float32, device="cuda")
+    ws = uw.Workspace(uw.epilogue_workspace_bytes(dm, x.shape[0]))
+    uw.gemm_epilogue(dm, to_dev(x), y, ws, activation=act)
+    ws.check()
+    ref, bound = epilogue_bound(bf16_f64(x), 0.0, 0.0, act, 0.0, False)
+    assert np.all(np.abs(y.cpu().numpy().astype(np.float64) - ref) <= bound)
 
 
 # --------------------------- streams and workspaces --------------------------

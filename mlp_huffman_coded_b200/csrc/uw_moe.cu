@@ -23,9 +23,9 @@ namespace {
 // so a token's place among them is a population count, whatever the order of
 // the atomics.
 //
-// A prompt takes two launches: the first chooses and counts per block, the
-// second adds up the counts of the blocks before it (at most kMaxRouteBlocks)
-// and places the tokens.  Up to 64 tokens take one block and one launch.
+// A prompt takes two launches: the first chooses, counts per block and finds
+// each choice's place among its block's, the second adds up the counts of the
+// blocks before it (at most kMaxRouteBlocks).  Up to 64 tokens take one block and one launch.
 // Launch latency bounds both: 8192 tokens x 64 experts are 1 MB of BF16 logits.
 constexpr int kRouteWarps = 16, kRouteThreads = 32 * kRouteWarps;
 constexpr int kRouteChunk = 64;       // tokens ranked together (two mask words)
@@ -174,9 +174,11 @@ __device__ __forceinline__ void scan_experts(const int32_t* total, int32_t* firs
   if (lane == 0) first[E] = base;
 }
 
-// Slots of the tokens [t0, t0 + n) from their masks and each expert's next
-// free slot (advanced afterwards by the caller).
-__device__ __forceinline__ void place(const RouteParams& p, int t0, int n, const uint32_t* masks, const int32_t* next) {
+// The places of the tokens [t0, t0 + n) among the choices of their experts,
+// from their masks and the choices counted before them.  FINAL: `base` holds
+// the experts' slots already, and the slots' tokens are noted.
+template <bool FINAL>
+__device__ __forceinline__ void place(const RouteParams& p, int t0, int n, const uint32_t* masks, const int32_t* base) {
   for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
     const int t = i / p.k;
     const int64_t at = static_cast<int64_t>(t0) * p.k + i;
@@ -184,9 +186,8 @@ __device__ __forceinline__ void place(const RouteParams& p, int t0, int n, const
     int slot = -1;
     if (e >= 0) {
       const uint32_t lo = masks[2 * e], hi = masks[2 * e + 1];
-      const int before = t < 32 ? __popc(lo & ((1u << t) - 1)) : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1));
-      slot = next[e] + before;
-      p.rows[slot] = t0 + t;
+      slot = base[e] + (t < 32 ? __popc(lo & ((1u << t) - 1)) : __popc(lo) + __popc(hi & ((1u << (t - 32)) - 1)));
+      if (FINAL) p.rows[slot] = t0 + t;
     }
     p.slots[at] = slot;
   }
@@ -218,6 +219,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     }
     __syncthreads();
     if constexpr (!ONE) {
+      place<false>(p, c, min(kRouteChunk, t1 - c), masks, total);
+      __syncthreads();
       for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
         total[e] += __popc(masks[2 * e]) + __popc(masks[2 * e + 1]);
         masks[2 * e] = masks[2 * e + 1] = 0;
@@ -231,23 +234,21 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     if (warp == 0) scan_experts(total, first, p.E, lane);
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
-    place(p, 0, p.T, masks, first);
+    place<true>(p, 0, p.T, masks, first);
   } else {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = total[e];
   }
 }
 
+// Adds up the counts of the blocks before this one and turns the places among
+// a block's choices into slots.
 __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams p) {
   extern __shared__ int32_t sh[];
-  uint32_t* masks = reinterpret_cast<uint32_t*>(sh);  // [E][2]
-  int32_t* total = sh + 2 * p.E;                      // [E]
-  int32_t* first = total + p.E;                       // [E + 1]
-  int32_t* before = first + p.E + 1;                  // [E] choices of earlier blocks
+  int32_t* total = sh;              // [E]
+  int32_t* first = total + p.E;     // [E + 1]
+  int32_t* base = first + p.E + 1;  // [E] choices of earlier blocks, then the block's first slots
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-    masks[2 * e] = masks[2 * e + 1] = 0;
-    total[e] = before[e] = 0;
-  }
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) total[e] = base[e] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
@@ -257,38 +258,31 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteParams 
   for (int i = threadIdx.x; i < parts * p.E; i += kRouteThreads) {
     const int e = i % p.E, part = i / p.E;
     int all = 0, earlier = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
       const int v = __ldcg(p.counts + static_cast<int64_t>(b) * p.E + e);
       all += v;
       if (b < static_cast<int>(blockIdx.x)) earlier += v;
     }
     atomicAdd(&total[e], all);
-    atomicAdd(&before[e], earlier);
+    atomicAdd(&base[e], earlier);
   }
   __syncthreads();
   if (warp == 0) scan_experts(total, first, p.E, lane);
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = first[e];
+  for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) {
+    if (blockIdx.x == 0) p.offsets[e] = first[e];
+    if (e < p.E) base[e] += first[e];
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) first[e] += before[e];
-  __syncthreads();
-  const int t0 = blockIdx.x * p.tokens_per_block, t1 = min(p.T, t0 + p.tokens_per_block);
-  for (int c = t0; c < t1; c += kRouteChunk) {
-    const int n = min(kRouteChunk, t1 - c);
-    for (int i = threadIdx.x; i < n * p.k; i += kRouteThreads) {
-      const int e = p.experts[static_cast<int64_t>(c) * p.k + i], t = i / p.k;
-      if (e >= 0) atomicOr(&masks[2 * e + (t >> 5)], 1u << (t & 31));
-    }
-    __syncthreads();
-    place(p, c, n, masks, first);
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-      first[e] += __popc(masks[2 * e]) + __popc(masks[2 * e + 1]);
-      masks[2 * e] = masks[2 * e + 1] = 0;
-    }
-    __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_block * p.k;
+  const int n = min(p.T - static_cast<int>(blockIdx.x) * p.tokens_per_block, p.tokens_per_block) * p.k;
+  for (int i = threadIdx.x; i < n; i += kRouteThreads) {
+    const int e = __ldcg(p.experts + i0 + i);
+    if (e < 0) continue;
+    const int slot = base[e] + __ldcg(p.slots + i0 + i);
+    p.slots[i0 + i] = slot;
+    p.rows[slot] = static_cast<int32_t>((i0 + i) / p.k);
   }
 }
 
@@ -348,7 +342,7 @@ uw_status launch_route(const RouteParams& p, const RoutePlan& r, cudaStream_t s)
   else if (p.E <= 256) st = launch_route_epl<32, 8>(p, r, s);
   else st = launch_route_epl<kMaxExperts / 32, 32>(p, r, s);
   if (st != UW_OK || r.blocks == 1) return st;
-  return launch_pdl(place_kernel, static_cast<unsigned>(r.blocks), kRouteThreads, static_cast<size_t>(5 * p.E + 1) * 4,
+  return launch_pdl(place_kernel, static_cast<unsigned>(r.blocks), kRouteThreads, static_cast<size_t>(3 * p.E + 1) * 4,
                     s, p);
 }
 

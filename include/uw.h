@@ -559,7 +559,9 @@ UW_API uw_status uw_experts_init(const uw_matrix* const* mats, int32_t n_experts
                                  size_t table_bytes, uw_experts* out, void* stream);
 
 /* Workspace of the grouped products for n_rows slots (0 for invalid
- * arguments); swiglu: nonzero for uw_gemm_grouped_swiglu. */
+ * arguments); swiglu: nonzero for uw_gemm_grouped_swiglu.  This size and the
+ * others of this part never fall with the number of rows, tokens or choices:
+ * a workspace for the largest batch serves every smaller one. */
 UW_API size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, int32_t swiglu);
 
 /* Matrix products grouped by expert with ragged sizes (the products of a

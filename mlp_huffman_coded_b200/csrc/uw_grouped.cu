@@ -1250,6 +1250,10 @@ struct GLayout {
   size_t smem = 0;
 };
 
+// The widest tile: what tensor memory and shared memory hold, and no more than
+// the rows there are.
+int most_columns(int n_rows, int nmat) { return std::min(nmat == 2 ? 192 : 256, (n_rows + 15) / 16 * 16); }
+
 // Columns per tile, at most: the width for which an estimate of the launch is
 // smallest, in units of one k-block of a tile (about 500 cycles).  Wide tiles
 // rebuild each weight tile less often, narrow ones give more tiles to spread
@@ -1272,7 +1276,7 @@ struct GLayout {
 // average 231 us at 16, 217 at 32; 64 rows 377 at 96, 267 at 128, 289 at 192).
 int pick_cap(int n_rows, int E, int nmat, int n_mt, int KB, int sms) {
   static const int kWidths[] = {16, 32, 48, 64, 96, 128, 160, 192, 224, 256};
-  const int most = std::min(nmat == 2 ? 192 : 256, (n_rows + 15) / 16 * 16);
+  const int most = most_columns(n_rows, nmat);
   const double groups = std::min(n_rows, E), avg = n_rows / groups;
   const double weights = nmat * groups * n_mt * KB;  // tiles of them
   int best = most;
@@ -1358,6 +1362,7 @@ struct GPlan {
 
 uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, bool scattered, int sms, GPlan* out) {
   if (E < 1 || E > kMaxExperts || n_rows < 0) return UW_ERR_INVALID_ARG;
+  if (n_rows > 0x7FFF * 256) return UW_ERR_UNSUPPORTED_SHAPE;  // column tiles in 15 bits (below)
   if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
   GPlan g;
   g.n_mt = static_cast<int>((N + 127) / 128);
@@ -1384,9 +1389,15 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   if (units > 0x7FFFFFFF || n_rows / g.lay.cap + 1 > 0x7FFF) return UW_ERR_UNSUPPORTED_SHAPE;
   g.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), sms));
   g.partial_stride = static_cast<size_t>(nmat) * 128 * g.lay.cap;
-  g.bytes = kWsHeader + kCounterBytes + align_up(2 * static_cast<size_t>(g.grid) * g.partial_stride * 4, 256);
-  if (scattered && g.lay.cap > kGatherCap) {
-    g.permuted = g.bytes;
+  // The workspace does not depend on the width that was picked, so that it
+  // never falls with n_rows: one for the largest batch serves every smaller one.
+  const int64_t most_units = std::min<int64_t>(n_rows, n_rows / 16 + E) * ((N + 127) / 128) * g.KB;
+  const int most1 = most_columns(n, 1), most2 = most_columns(n, 2);
+  const size_t columns = swiglu || most1 > kPairCap ? 2 * most2 : most1;
+  g.bytes = kWsHeader + kCounterBytes +
+            align_up(2 * static_cast<size_t>(std::min<int64_t>(most_units, sms)) * 128 * columns * 4, 256);
+  if (scattered && most1 > kGatherCap) {
+    if (g.lay.cap > kGatherCap) g.permuted = g.bytes;
     g.bytes += align_up(static_cast<size_t>(n_rows) * K * 2, 256);
   }
   *out = g;

@@ -317,7 +317,9 @@ bool route_plan(int64_t T, int64_t E, int64_t k, RoutePlan* out) {
   const int64_t per = (chunks + kMaxRouteBlocks - 1) / kMaxRouteBlocks;
   r.tokens_per_block = static_cast<int>(per * kRouteChunk);
   r.blocks = static_cast<int>((chunks + per - 1) / per);
-  r.bytes = kWsHeader + kCounterBytes + (r.blocks > 1 ? align_up(static_cast<size_t>(r.blocks) * E * 4, 256) : 0);
+  // (the blocks that the counts have room for never fall with T)
+  const int64_t most = std::min<int64_t>(chunks, kMaxRouteBlocks);
+  r.bytes = kWsHeader + kCounterBytes + (most > 1 ? align_up(static_cast<size_t>(most) * E * 4, 256) : 0);
   *out = r;
   return true;
 }

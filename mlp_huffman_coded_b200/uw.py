@@ -662,18 +662,26 @@ def gemm_grouped_swiglu(gate: Experts, up: Experts, x, offsets, h, ws: Workspace
 
 
 class Route:
-    """Where uw_moe_route leaves its results (torch tensors own memory)."""
+    """Where uw_moe_route leaves its results (torch tensors own memory).  The
+    tensors stay the same for the object's life: their addresses are taken
+    once."""
 
     def __init__(self, n_tokens: int, n_experts: int, top_k: int, device="cuda"):
         import torch
         self.n_tokens, self.n_experts, self.top_k = n_tokens, n_experts, top_k
-        self.weights = torch.empty(n_tokens, top_k, dtype=torch.float32, device=device)
-        self.experts = torch.empty(n_tokens, top_k, dtype=torch.int32, device=device)
-        self.slots = torch.empty(n_tokens, top_k, dtype=torch.int32, device=device)
-        self.rows = torch.empty(n_tokens * top_k, dtype=torch.int32, device=device)
-        self.offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=device)
+        self._tensors = (torch.empty(n_tokens, top_k, dtype=torch.float32, device=device),
+                         torch.empty(n_tokens, top_k, dtype=torch.int32, device=device),
+                         torch.empty(n_tokens, top_k, dtype=torch.int32, device=device),
+                         torch.empty(n_tokens * top_k, dtype=torch.int32, device=device),
+                         torch.empty(n_experts + 1, dtype=torch.int32, device=device))
         self.device = self.weights.get_device()
-        self.addresses = tuple(t.data_ptr() for t in (self.weights, self.experts, self.slots, self.rows, self.offsets))
+        self.addresses = tuple(t.data_ptr() for t in self._tensors)
+
+    weights = property(lambda self: self._tensors[0])
+    experts = property(lambda self: self._tensors[1])
+    slots = property(lambda self: self._tensors[2])
+    rows = property(lambda self: self._tensors[3])
+    offsets = property(lambda self: self._tensors[4])
 
 
 def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:

@@ -267,6 +267,22 @@ def test_block_equals_its_four_calls(sparse_mlp):
     assert torch.equal(y, y2)
 
 
+def test_a_workspace_for_the_largest_batch_serves_smaller_ones(sparse_mlp):
+    import torch
+    _, ex = sparse_mlp
+    E, d, k = len(ex[0]), ex[2].rows, 2
+    big = uw.Workspace(uw.moe_workspace_bytes(*ex, 400, k))
+    for T in (400, 1, 30, 33, 70, 129, 200, 399):
+        x, logits = to_dev(synth.activations(T, d, 680)), torch.randn(T, E, device="cuda")
+        y, z = empty_bf16(T, d), empty_bf16(T, d)
+        own = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+        uw.moe_block(*ex, x, logits, k, y, big)
+        uw.moe_block(*ex, x, logits, k, z, own)
+        big.check()
+        own.check()
+        assert torch.equal(y, z), T
+
+
 def test_layers_chained_on_one_stream_match_layers_one_by_one(sparse_mlp):
     """Launches overlap (a kernel starts while the one before it finishes);
     ten blocks in a row, in place on the residual stream, equal the same

@@ -52,11 +52,41 @@ def test_workspace_sizes():
     assert f(None, 8, 0) == 0 and f(C.byref(t), -1, 0) == 0
     assert f(C.byref(table(n=0)), 8, 0) == 0 and f(C.byref(table(n=2000)), 8, 0) == 0
     assert f(C.byref(table(cols=500)), 8, 0) == 0 and f(C.byref(table(cols=1 << 16)), 8, 0) == 0
+    for n_rows in (1 << 30, (1 << 31) - 15, (1 << 31) - 1):
+        assert f(C.byref(t), n_rows, 0) == f(C.byref(t), n_rows, 1) == 0
     # more units than an index holds
     assert f(C.byref(table(rows=1 << 20, cols=32768)), 1 << 22, 0) == 0
     g = uw.lib().uw_gemm_epilogue_workspace_bytes
     L = matrix().L
     assert g(C.byref(L), 1) > 0 and g(C.byref(L), 100000) > 0 and g(C.byref(L), -1) == 0 and g(None, 1) == 0
+
+
+@pytest.mark.parametrize("n,rows,cols", [(1, 4096, 4096), (1, 14336, 4096), (8, 4096, 14336), (64, 2048, 1024),
+                                         (8, 200, 192), (700, 1, 64)])
+def test_a_workspace_for_more_rows_serves_fewer(n, rows, cols):
+    lib = uw.lib()
+    gate, down = table(n, rows, cols), table(n, 64 * -(-cols // 64), 64 * -(-rows // 64))
+    up_to = [*range(1, 300), 511, 512, 513, 1000, 2048, 4096, 4097, 8192, 8193, 8256, 20000]
+    for swiglu in (0, 1):
+        sizes = [lib.uw_grouped_workspace_bytes(C.byref(gate), r, swiglu) for r in up_to]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+    L = uw.Layout()
+    L.rows, L.cols = rows, cols
+    sizes = [lib.uw_gemm_epilogue_workspace_bytes(C.byref(L), r) for r in up_to]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    k = min(2, n)
+    sizes = [lib.uw_moe_route_workspace_bytes(r, n, k) for r in up_to]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    if rows % 64 == 0:
+        sizes = [lib.uw_moe_workspace_bytes(C.byref(gate), C.byref(gate), C.byref(down), r, k) for r in up_to]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+def test_route_tensors_are_not_replaced():
+    route = uw.Route(3, 4, 2, device="cpu")
+    for name in ("weights", "experts", "slots", "rows", "offsets"):
+        with pytest.raises(AttributeError):
+            setattr(route, name, None)
 
 
 def test_route_sizes():

@@ -1263,11 +1263,10 @@ int most_columns(int n_rows, int nmat) { return std::min(nmat == 2 ? 192 : 256, 
 // weights outgrow L2: their column tiles then come at different times); a
 // tile's epilogue 0.7 per 8 columns and 2, behind the next tile's k-blocks
 // where there are two accumulators, a quarter of that for the last one of a
-// CTA; sharing a tile out the writing (half of
-// that), a ticket and the adding up of the parts, which 6 groups of warps do 8
-// columns each at a time.  A wider tile has to win by 3%: it takes shared
-// memory from the weight ring.  Measured against the widest
-// tile: 512 rows of 1024 x 1024 8.0 us at 64 columns, 15.2 at 256; 128 rows of
+// CTA; sharing a tile out the writing (half of that), a ticket and the adding up
+// of the parts, which 6 groups of warps do 8 columns each at a time.  A wider
+// tile has to win by 3%: it takes shared memory from the weight ring.
+// Measured against the widest tile: 512 rows of 1024 x 1024 8.0 us at 64 columns, 15.2 at 256; 128 rows of
 // 1024 x 4096 11.8 at 32, 23.3 at 128; 450 rows of 5896 x 1088 15.6 at 160,
 // 17.9 at 240; but 1000 rows of 4096 x 4096 38.5 at 256, 51.5 at 176.
 // Groups of several experts vary in size: an average group of `avg` rows is

@@ -574,8 +574,9 @@ def _call(name, device, stream, *args):
 
 class Experts:
     """One compressed matrix per expert (same shape, direct-palette form), as
-    the grouped products take them (uw_experts_init).  Keeps the matrices;
-    their direct-palette form must not be prepared again afterwards."""
+    the grouped products take them (uw_experts_init).  The device table holds
+    addresses, so the tensors of that form are kept: a matrix may be prepared
+    again or dropped, and the products go on with the form it had here."""
 
     def __init__(self, matrices, stream=None):
         _need_torch()
@@ -586,6 +587,7 @@ class Experts:
         if any(m.sm.get_device() != self.device for m in self.matrices):
             raise UwError(UW_ERR_INVALID_ARG, "Experts: matrices on different devices")
         n = len(self.matrices)
+        self._packs = [(m.pack, m.pack_off) for m in self.matrices]
         nbytes = int(lib().uw_experts_table_bytes(n))
         self.table = _torch.empty(max(nbytes, 16), dtype=_torch.uint8, device=f"cuda:{self.device}")
         self.c = ExpertTable()

@@ -257,6 +257,25 @@ def test_larger_swiglu_against_float64(rows, cols, counts):
     assert worst_excess(h, gs, x, r, off, cols, swiglu_with=us) <= 0
 
 
+def test_matrices_prepared_again_leave_the_products_as_they_were():
+    """A matrix's new pack gets new memory and the old one's would be handed
+    out again: Experts keeps it."""
+    import torch
+    mats = expert_weights(3, 512, 1024, 935)
+    ex = experts_of(mats)
+    off = offsets_of([5, 0, 30])
+    x = synth.activations(35, 1024, 936)
+    want = run_grouped(ex, x, off, 35)
+    ws = uw.Workspace(256)
+    sizes = [m.pack.numel() for m in ex.matrices]
+    for m in ex.matrices:
+        m.prepare_direct_palette(ws, keep_idx4=False)
+    torch.cuda.synchronize()
+    taken = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    assert np.array_equal(run_grouped(ex, x, off, 35), want)
+    del taken
+
+
 def test_six_hundred_experts():
     mats = expert_weights(6, 128, 64, 930)
     dms = [device_matrix(m) for m in mats]

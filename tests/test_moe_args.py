@@ -160,6 +160,43 @@ def test_experts_refusals():
         uw.Experts([])
 
 
+def test_experts_keep_the_tensors_their_table_points_to(monkeypatch):
+    """Preparing a matrix again replaces its pack; the table still holds the
+    old one's address, so Experts has to keep it alive."""
+    import gc
+    import weakref
+
+    import torch
+
+    class Prepared:  # the parts of a DeviceMatrix that Experts takes
+        class sm:
+            get_device = staticmethod(lambda: 0)
+
+        def __init__(self):
+            self.mat = uw.Matrix()
+            self.prepare_direct_palette()
+
+        def prepare_direct_palette(self):
+            self.pack, self.pack_off = torch.zeros(64, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+
+    uw._need_torch()
+    monkeypatch.setattr(uw, "_call", lambda *a: None)
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: real(*a, **k))
+    mats = [Prepared(), Prepared()]
+    kept = [weakref.ref(t) for m in mats for t in (m.pack, m.pack_off)]
+    ex = uw.Experts(mats)
+    for m in mats:
+        m.prepare_direct_palette()
+    del m
+    mats.clear()
+    gc.collect()
+    assert len(ex) == 2 and all(r() is not None for r in kept)
+    del ex
+    gc.collect()
+    assert all(r() is None for r in kept)
+
+
 def test_route_and_combine_refusals():
     lib = uw.lib()
 

@@ -735,8 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = e0 + lane;
       int a = 0, b = 0;
       if (e < p.E) {
-        a = p.offsets ? p.offsets[e] : 0;
-        b = p.offsets ? p.offsets[e + 1] : p.n_rows;
+        // through L2: with `early` no wait stands between the kernel that
+        // wrote them and these reads, so L1 may hold the previous routing's
+        a = p.offsets ? __ldcg(p.offsets + e) : 0;
+        b = p.offsets ? __ldcg(p.offsets + e + 1) : p.n_rows;
       }
       // offsets that leave [0, n_rows] or fall: nothing is computed
       bad |= a < 0 || b < a || b > p.n_rows;

@@ -312,6 +312,38 @@ def test_layers_chained_on_one_stream_match_layers_one_by_one(sparse_mlp):
         assert torch.equal(fast[0], slow[0]) and torch.equal(fast[1], slow[1])
 
 
+@pytest.mark.parametrize("T", [9, 30, 150, 700])
+def test_every_call_of_a_chain_sees_its_own_routing(sparse_mlp, T):
+    """Twelve blocks in a row on one workspace, each with a routing of its
+    own, against the same calls with the device idle between them.  From 9
+    tokens on the rows of x are copied next to each other first, so both
+    products read the groups before they wait for the kernel ahead."""
+    import torch
+    _, ex = sparse_mlp
+    k, d, E, n = 2, ex[2].rows, len(ex[0]), 12
+    x = to_dev(synth.activations(T, d, 685))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    # each call prefers other experts: groups of very different sizes
+    logits = torch.randn(n, T, E, device="cuda", generator=g) + 4 * torch.randn(n, 1, E, device="cuda", generator=g)
+    logits[5] = -math.inf  # no group has a slot
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+
+    def chain(sync):
+        ys = [empty_bf16(T, d) for _ in range(n)]
+        for l, y in zip(logits, ys):
+            uw.moe_block(*ex, x, l, k, y, ws)
+            if sync:
+                torch.cuda.synchronize()
+        ws.check()
+        return ys
+
+    slow = chain(True)
+    assert not bool(slow[5].any()) and not torch.equal(slow[0], slow[1])
+    for _ in range(5):
+        for a, b in zip(chain(False), slow):
+            assert torch.equal(a, b)
+
+
 def test_captured_block_replays_on_new_inputs(sparse_mlp):
     """Routing is on the device, so one captured graph serves every batch of
     its size, whatever its groups; on another stream than the default."""

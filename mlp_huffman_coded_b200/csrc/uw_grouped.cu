@@ -416,13 +416,17 @@ __device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
 // ------------------------------- epilogue ------------------------------------
 // FP32 throughout; the only rounding is the store's.  The GELU forms are
 // written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
-// Divisions are the fast ones (2 units in the last place; 0 where exp
-// overflows the range, as the limit is).
+// Divisions are the fast ones (2 units in the last place for divisors below
+// 2^126; theirs are at most 2).
+// v / (1 + exp(-t)) for v and t of one sign, from e = exp(-|t|): exp(-t) leaves
+// the range where the result is still a normal number (SiLU(-90) = -7.4e-38).
+__device__ __forceinline__ float times_sigmoid(float v, float t, float e) {
+  return __fdividef(t > 0.0f ? v : v * e, 1.0f + e);
+}
+
 // SiLU(v) for a product that is rounded to BF16 next: the fast exponential
-// (relative error about 2^-24 (2 + 1.2 |v|), far below BF16's 2^-9 wherever
-// the result is not negligible) and the fast division (2 units in the last
-// place; 0 where exp(-v) overflows, as the limit is).
-__device__ __forceinline__ float silu_fast(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+// (relative error at most 2^-23 (2 + 1.2 |v|), far below BF16's 2^-8).
+__device__ __forceinline__ float silu_fast(float v) { return times_sigmoid(v, v, __expf(-fabsf(v))); }
 
 // Phi(-a) = erfc(a / sqrt 2) / 2 for a >= 0, as exp(-a^2 / 2) t P(t) with
 // z = a / sqrt 2, t = 1 / (1 + z / 2).  P: a minimax fit of erfcx(z) / t on z
@@ -462,12 +466,12 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float t = 1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]);  // 2 sqrt(2 / pi) (...)
-        v[j] = __fdividef(v[j], 1.0f + expf(-t));
+        v[j] = times_sigmoid(v[j], t, expf(-fabsf(t)));
       }
       break;
     case UW_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = __fdividef(v[j], 1.0f + expf(-v[j]));
+      for (int j = 0; j < N; ++j) v[j] = times_sigmoid(v[j], v[j], expf(-fabsf(v[j])));
       break;
     default: break;
   }

@@ -59,6 +59,46 @@ def epilogue_bound(v, dv, bias, act, residual, bf16):
     return y, dy + 1e-30
 
 
+SMALLEST_NORMAL = 2.0 ** -126
+
+
+def act_tail(v, name):
+    """act_f64 in forms that keep their relative accuracy for negative v,
+    where 1 + tanh would cancel."""
+    v = np.asarray(v, dtype=np.float64)
+    if name != "gelu_tanh":
+        return act_f64(v, name)
+    t = 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    with np.errstate(over="ignore"):
+        return v / (1 + np.exp(-t))
+
+
+def activation_bound(v, name):
+    """Largest error of an FP32 activation of an exact v, relative to the
+    activation itself; below the smallest normal number nothing is promised.
+    u = 2^-24 is one FP32 rounding; a unit in the last place is at most 2 u.
+
+    SiLU, (v or v e) / (1 + e) with e = exp(-|v|): e 2 units (4 u), v e 1 u,
+    1 + e 1 u and half of e's error, the quotient 2 units (4 u): 12 u.
+    GELU's tanh form, the same with t, which is off by 7 u relative (three
+    products, a sum, two rounded constants and their product), so e by
+    another 7 u |t|, and the divisor by half of that.
+    GELU, v Phi(v) with Phi(-a) = exp(-a^2 / 2) t P(t) / 2: t 7 u (divisor 3 u,
+    quotient 4 u), and t P(t) changes by at most 2.3 times as much; P 9
+    roundings of terms whose magnitudes add up to 2.2 times P, and the fit's
+    1 u; the products 4 u; the fast exponential of x = -v^2 / 2 is off by
+    2 + 1.173 |x| units, and the rounding of x gives another |x| u."""
+    v = np.asarray(v, dtype=np.float64)
+    y = np.abs(act_tail(v, name))
+    if name == "gelu":
+        rel = 48 + 1.7 * v * v
+    elif name == "gelu_tanh":
+        rel = 13 + 11 * np.abs(2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3))
+    else:
+        rel = np.full_like(v, 13.0 if name == "silu" else 0.0)
+    return np.minimum(rel * F32, 1.0) * y + SMALLEST_NORMAL
+
+
 def product(w, x):
     """x W^T in float64 and sum |w x| (BF16 bit patterns in)."""
     wf, xf = O.bf16_to_f64(w), O.bf16_to_f64(x)

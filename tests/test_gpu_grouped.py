@@ -9,7 +9,8 @@ from mlp_huffman_coded_b200 import uw
 from oracle import uw_oracle as O
 
 from gpu_util import bf16_f64, device_matrix, empty_bf16, to_dev, to_host_u16
-from moe_util import check_slots, epilogue_bound, expert_weights, grouped_ref, swiglu_ref
+from moe_util import (F32, HALF_ULP, SMALLEST_NORMAL, act_tail, activation_bound, check_slots, epilogue_bound,
+                      expert_weights, grouped_ref, swiglu_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -353,6 +354,50 @@ def test_activations_over_their_range(act):
     ws.check()
     ref, bound = epilogue_bound(bf16_f64(x), 0.0, 0.0, act, 0.0, False)
     assert np.all(np.abs(y.cpu().numpy().astype(np.float64) - ref) <= bound)
+
+
+@pytest.mark.parametrize("act", sorted(uw.ACTIVATIONS))
+def test_activations_keep_their_relative_accuracy(act):
+    """The same products against bounds relative to the activation: the tails
+    of negative values, down to the smallest normal number."""
+    import torch
+    bits = np.arange(0x0080, 0x4300, dtype=np.uint16)  # 2^-126 .. 128
+    x = np.concatenate([bits, bits | 0x8000])
+    x = np.resize(x, -(-x.size // 64) * 64).reshape(-1, 64)
+    dm = device_matrix(synth.f32_to_bf16_bits(np.eye(64, dtype=np.float32)))
+    y = torch.empty(x.shape[0], 64, dtype=torch.float32, device="cuda")
+    ws = uw.Workspace(uw.epilogue_workspace_bytes(dm, x.shape[0]))
+    uw.gemm_epilogue(dm, to_dev(x), y, ws, activation=act)
+    ws.check()
+    v = bf16_f64(x)
+    off = np.abs(y.cpu().numpy().astype(np.float64) - act_tail(v, act)) / activation_bound(v, act)
+    assert off.max() <= 1, (float(off.max()), float(v.ravel()[off.argmax()]))
+
+
+def test_swiglu_over_the_range_of_the_gate():
+    """Gate = identity, up = 2^20 times it: h = SiLU(x) x 2^20 for every BF16 x
+    of up to 128.  Relative error of SiLU in units of 2^-24: a fast exponential
+    is off by 4 + 2.4 |x| at most (2 + 1.173 |x| units in the last place), its
+    argument's rounding by |x| and a few for a scale; the divisor and the
+    products take 1 to 4 each; BF16 rounds once more."""
+    eye = np.eye(64, dtype=np.float32)
+    gate, up = (experts_of([synth.f32_to_bf16_bits(m)]) for m in (eye, eye * 2.0 ** 20))
+    bits = np.arange(0x0080, 0x4300, dtype=np.uint16)
+    x = np.concatenate([bits, bits | 0x8000])
+    x = np.resize(x, -(-x.size // 64) * 64).reshape(-1, 64)
+    h = empty_bf16(*x.shape)
+    ws = uw.Workspace(uw.grouped_workspace_bytes(gate, x.shape[0], swiglu=True))
+    uw.gemm_grouped_swiglu(gate, up, to_dev(x), to_dev(offsets_of([x.shape[0]])), h, ws)
+    ws.check()
+    v = bf16_f64(x)
+    silu = act_tail(v, "silu")
+    ref = silu * v * 2.0 ** 20
+    rel = np.minimum((13 + 3.6 * np.abs(v)) * F32, 1.0)
+    # (a SiLU below the smallest normal number is held to that only)
+    d = rel * np.abs(ref) + SMALLEST_NORMAL * np.abs(v) * 2.0 ** 20
+    bound = d + HALF_ULP * (np.abs(ref) + d) + 2.0 ** -133
+    off = np.abs(bf16_f64(to_host_u16(h)) - ref) / bound
+    assert off.max() <= 1, (float(off.max()), float(v.ravel()[off.argmax()]))
 
 
 # --------------------------- streams and workspaces --------------------------

@@ -8,7 +8,7 @@ import pytest
 from mlp_huffman_coded_b200 import synth
 from mlp_huffman_coded_b200 import uw
 
-from moe_util import act_f64, route_ref
+from moe_util import act_f64, act_tail, activation_bound, route_ref
 
 P = 0x10000  # a non-NULL, aligned address that no call may reach
 
@@ -271,3 +271,21 @@ def test_the_plain_forms_themselves():
     w, e, s, rows, off = route_ref(np.array([[0.0, 1.0, 1.0], [5.0, -np.inf, np.nan]], np.float32), 2)
     assert e.tolist() == [[1, 2], [0, -1]] and w.tolist() == [[0.5, 0.5], [1.0, 0.0]]
     assert s.tolist() == [[1, 2], [0, -1]] and rows.tolist() == [1, 0, 0] and off.tolist() == [0, 1, 2, 3]
+
+
+def test_the_activations_bounds_tell_lost_tails_apart():
+    """Forms that cancel, overflow or cut off for negative values break the
+    bounds that the kernels' FP32 results are held to."""
+    v = synth.bf16_bits_to_f32((np.arange(0x0080, 0x4300, dtype=np.uint16) | 0x8000))  # -2^-126 .. -128
+    f, d = np.float32, v.astype(np.float64)
+    from math import erf, pi, sqrt
+    with np.errstate(all="ignore"):
+        cancelling = {"gelu": f(0.5) * v * (f(1) + np.array([erf(t / sqrt(2)) for t in d], f)),
+                      "gelu_tanh": f(0.5) * v * (f(1) + np.tanh(f(sqrt(2 / pi)) * (v + f(0.044715) * v * v * v))),
+                      "silu": v / (f(1) + np.exp(-v))}  # exp overflows from -89 on
+    for act, y in cancelling.items():
+        ref, bound = act_tail(d, act), activation_bound(d, act)
+        assert np.all(np.abs(ref.astype(f) - ref) <= bound)
+        assert np.any(np.abs(y - ref) > bound), act
+        cut = np.where(np.abs(ref) < 1e-36, 0.0, ref)
+        assert np.any(np.abs(cut - ref) > bound), act

@@ -576,6 +576,8 @@ UW_API size_t uw_grouped_workspace_bytes(const uw_experts* w, int32_t n_rows, in
  * (plain BF16 product).  Slots outside [offsets[0], offsets[n_experts]) are
  * left as they were.  The matrix of an expert without slots is not read.
  * n_rows = 0 launches nothing.  y overlaps neither x nor rows nor offsets.
+ * n_rows up to UW_MAX_SLOTS is taken (more may be), as long as
+ * (n_rows / 192 + n_experts) * ceil(rows / 128) * (cols / 64) < 2^31.
  * Sums are FP32; their order depends only on the shapes, n_rows, the offsets
  * and the SM count.  cols <= 32768.
  * The table and the matrices are constant (see the conventions above);

@@ -1260,6 +1260,13 @@ struct GLayout {
 // the rows there are.
 int most_columns(int n_rows, int nmat) { return std::min(nmat == 2 ? 192 : 256, (n_rows + 15) / 16 * 16); }
 
+// Whether the schedule's indices hold every split of n_rows into E groups at
+// this width: column tiles of a group in 15 bits, k-blocks of all tiles in 31.
+bool schedule_fits(int n_rows, int E, int cap, int n_mt, int KB) {
+  const int64_t tiles = std::min<int64_t>(n_rows, n_rows / cap + E);
+  return n_rows / cap + 1 <= 0x7FFF && tiles * n_mt * KB <= 0x7FFFFFFF;
+}
+
 // Columns per tile, at most: the width for which an estimate of the launch is
 // smallest, in units of one k-block of a tile (about 500 cycles).  Wide tiles
 // rebuild each weight tile less often, narrow ones give more tiles to spread
@@ -1296,6 +1303,8 @@ int pick_cap(int n_rows, int E, int nmat, int n_mt, int KB, int sms) {
     } else if (cap < std::min(32, most)) {
       continue;
     }
+    // (millions of rows need wide tiles; grouped_plan refuses what none holds)
+    if (width < most && !schedule_fits(n_rows, E, cap, n_mt, KB)) continue;
     const double tiles = groups * n_mt * cols, chunks = std::max(1.0, avg / cols / 8), waves = std::ceil(tiles / sms);
     const double main = KB * nmat * std::max(0.7, std::min<double>(cap, avg / cols + 15) * 0.004);
     const double epi = 0.7 * chunks * nmat + 2;
@@ -1367,7 +1376,7 @@ struct GPlan {
 
 uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, bool scattered, int sms, GPlan* out) {
   if (E < 1 || E > kMaxExperts || n_rows < 0) return UW_ERR_INVALID_ARG;
-  if (n_rows > 0x7FFF * 256) return UW_ERR_UNSUPPORTED_SHAPE;  // column tiles in 15 bits (below)
+  if (n_rows > 0x7FFF * 256) return UW_ERR_UNSUPPORTED_SHAPE;  // (below; and the sums here stay in range)
   if (N < 1 || K < 64 || K % 64 != 0 || K > 32768 || N > (int64_t(1) << 31) - 128) return UW_ERR_UNSUPPORTED_SHAPE;
   GPlan g;
   g.n_mt = static_cast<int>((N + 127) / 128);
@@ -1383,7 +1392,8 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   const int cap2 = pick_cap(n, E, 2, swiglu ? g.n_mt : (g.n_mt + 1) / 2, g.KB, sms);
   const int64_t pair_units =
       static_cast<int64_t>((g.n_mt + 1) / 2) * std::max<int64_t>(E > 1 ? std::min(n_rows, E) : 1, n_rows / cap2) * g.KB;
-  g.pair = !swiglu && g.n_mt > 1 && cap > kPairCap && pair_units >= static_cast<int64_t>(kPairUnits) * sms;
+  g.pair = !swiglu && g.n_mt > 1 && cap > kPairCap && pair_units >= static_cast<int64_t>(kPairUnits) * sms &&
+           schedule_fits(n_rows, E, cap2, (g.n_mt + 1) / 2, g.KB);
   const int nmat = swiglu || g.pair ? 2 : 1;
   if (nmat == 2) cap = cap2;
   if (g.pair) g.n_mt = (g.n_mt + 1) / 2;
@@ -1391,7 +1401,7 @@ uw_status grouped_plan(int64_t N, int64_t K, int E, int n_rows, bool swiglu, boo
   // the most units any split of n_rows into E groups can give
   const int64_t tiles = std::min<int64_t>(n_rows, n_rows / g.lay.cap + E);
   const int64_t units = tiles * g.n_mt * g.KB;
-  if (units > 0x7FFFFFFF || n_rows / g.lay.cap + 1 > 0x7FFF) return UW_ERR_UNSUPPORTED_SHAPE;
+  if (!schedule_fits(n_rows, E, g.lay.cap, g.n_mt, g.KB)) return UW_ERR_UNSUPPORTED_SHAPE;
   g.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(units, 1), sms));
   g.partial_stride = static_cast<size_t>(nmat) * 128 * g.lay.cap;
   // The workspace does not depend on the width that was picked, so that it

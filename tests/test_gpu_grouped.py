@@ -307,6 +307,34 @@ def test_more_than_two_to_the_31_output_values():
     del y
 
 
+def test_millions_of_rows_of_a_small_matrix():
+    """More rows than the narrow tiles that such a matrix prefers can count."""
+    import torch
+    rows, cols, n = 200, 128, 2_600_003
+    mats = expert_weights(2, rows, cols, 945)
+    ups = expert_weights(2, rows, cols, 947)
+    ex, eu = experts_of(mats), experts_of(ups)
+    x = np.resize(synth.activations(4099, cols, 946), (n, cols))
+    xd, off = to_dev(x), offsets_of([700_001, n - 700_001])
+    y = torch.empty(n, rows, dtype=torch.bfloat16, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, n, swiglu=True))
+    spans = [(0, 300, 0), (700_001 - 260, 700_001, 0), (700_001, 700_300, 1), (2**21 - 100, 2**21 + 100, 1), (n - 300, n, 1)]
+    uw.gemm_grouped(ex, xd, to_dev(off), y, ws)
+    ws.check()
+    for a, b, e in spans:
+        assert worst_excess(y[a:b], [mats[e]], x[a:b], np.arange(b - a), [0, b - a], cols) <= 0
+    back = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")  # rows of x in falling order
+    uw.gemm_grouped_swiglu(ex, eu, xd, to_dev(off), y, ws, rows=back)
+    ws.check()
+    for a, b, e in spans:
+        assert worst_excess(y[a:b], [mats[e]], x[n - b:n - a][::-1].copy(), np.arange(b - a), [0, b - a], cols,
+                            swiglu_with=[ups[e]]) <= 0
+    uw.gemm_epilogue(ex.matrices[1], xd, y, ws)
+    ws.check()
+    for a, b, _ in spans:
+        assert worst_excess(y[a:b], [mats[1]], x[a:b], np.arange(b - a), [0, b - a], cols) <= 0
+
+
 # ------------------------------ special values -------------------------------
 
 def test_nan_and_infinite_activations_stay_in_their_slot():

@@ -82,6 +82,21 @@ def test_a_workspace_for_more_rows_serves_fewer(n, rows, cols):
         assert sizes[0] > 0 and sizes == sorted(sizes)
 
 
+@pytest.mark.parametrize("n,rows,cols", [(1, 200, 128), (1, 1, 64), (2, 64, 128), (8, 2048, 128), (64, 128, 512), (1024, 200, 128),
+                                         (3, 4096, 4096)])
+def test_every_batch_up_to_the_largest_is_taken(n, rows, cols):
+    lib, most = uw.lib(), 1 << 22
+    assert (most // 192 + n) * -(-rows // 128) * (cols // 64) < 1 << 31
+    up_to = sorted({most, most - 1, *(int(1.07 ** i) for i in range(1, 226))})
+    t, L = table(n, rows, cols), uw.Layout()
+    L.rows, L.cols = rows, cols
+    for swiglu in (0, 1):
+        sizes = [lib.uw_grouped_workspace_bytes(C.byref(t), r, swiglu) for r in up_to]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
+    sizes = [lib.uw_gemm_epilogue_workspace_bytes(C.byref(L), r) for r in up_to]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
 def test_route_tensors_are_not_replaced():
     route = uw.Route(3, 4, 2, device="cpu")
     for name in ("weights", "experts", "slots", "rows", "offsets"):

@@ -533,10 +533,25 @@ def _tensor(t, what, types, shape, device):
     return t.data_ptr()
 
 
+_INT32_MAX = 2**31 - 1
+
+
+def _count(n, what):
+    """A count that the library takes in 32 bits (ctypes would wrap it)."""
+    if not 0 <= n <= _INT32_MAX:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: {n} is not a count of at most 2^31 - 1")
+    return n
+
+
+def _size_arg(n):
+    """The same for the workspace sizes, which are 0 for what is too large."""
+    return max(-1, min(n, _INT32_MAX))
+
+
 def _matrix_of(t, what):
     """[rows, cols] of a 2-D tensor argument."""
-    if t is None or t.dim() != 2:
-        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a 2-D tensor is wanted")
+    if t is None or t.dim() != 2 or t.shape[0] > _INT32_MAX:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a 2-D tensor of fewer than 2^31 rows is wanted")
     return t.shape
 
 
@@ -544,6 +559,8 @@ def _out_type(t, what):
     """(uw_out_type, element types) of a BF16 or FP32 tensor."""
     if _torch is None:
         _need_torch()
+    if t is None:
+        raise UwError(UW_ERR_INVALID_ARG, f"{what}: a tensor is wanted")
     if t.dtype in _BF16:
         return OUT_BF16, _BF16
     if t.dtype in _FP32:
@@ -600,12 +617,12 @@ class Experts:
 
 
 def grouped_workspace_bytes(experts: Experts, n_rows: int, swiglu: bool = False) -> int:
-    return int(lib().uw_grouped_workspace_bytes(C.byref(experts.c), n_rows, int(swiglu)))
+    return int(lib().uw_grouped_workspace_bytes(C.byref(experts.c), _size_arg(n_rows), int(swiglu)))
 
 
 def epilogue_workspace_bytes(dm_or_layout, batch: int) -> int:
     L = dm_or_layout.mat.L if isinstance(dm_or_layout, DeviceMatrix) else dm_or_layout
-    return int(lib().uw_gemm_epilogue_workspace_bytes(C.byref(L), batch))
+    return int(lib().uw_gemm_epilogue_workspace_bytes(C.byref(L), _size_arg(batch)))
 
 
 def _epilogue(device, bias_shape, n_rows, rows, y, bias, activation, residual):
@@ -670,7 +687,7 @@ class Route:
 
     def __init__(self, n_tokens: int, n_experts: int, top_k: int, device="cuda"):
         import torch
-        self.n_tokens, self.n_experts, self.top_k = n_tokens, n_experts, top_k
+        self.n_tokens, self.n_experts, self.top_k = (_count(n, "Route") for n in (n_tokens, n_experts, top_k))
         self._tensors = (torch.empty(n_tokens, top_k, dtype=torch.float32, device=device),
                          torch.empty(n_tokens, top_k, dtype=torch.int32, device=device),
                          torch.empty(n_tokens, top_k, dtype=torch.int32, device=device),
@@ -687,7 +704,7 @@ class Route:
 
 
 def route_workspace_bytes(n_tokens: int, n_experts: int, top_k: int) -> int:
-    return int(lib().uw_moe_route_workspace_bytes(n_tokens, n_experts, top_k))
+    return int(lib().uw_moe_route_workspace_bytes(_size_arg(n_tokens), _size_arg(n_experts), _size_arg(top_k)))
 
 
 def moe_route(logits, route: Route, ws: Workspace, renormalize: bool = True, stream=None):
@@ -704,6 +721,7 @@ def moe_combine(parts, slots, weights, y, residual=None, stream=None):
     (uw_moe_combine): parts FP32 or BF16 [n_rows, cols]."""
     n_rows, cols = _matrix_of(parts, "parts")
     n_tokens, top_k = _matrix_of(slots, "slots")
+    _count(top_k, "top_k")
     dev = parts.get_device()
     typ, types = _out_type(parts, "parts")
     _call("uw_moe_combine", dev, stream,
@@ -714,7 +732,8 @@ def moe_combine(parts, slots, weights, y, residual=None, stream=None):
 
 
 def moe_workspace_bytes(gate: Experts, up: Experts, down: Experts, n_tokens: int, top_k: int) -> int:
-    return int(lib().uw_moe_workspace_bytes(C.byref(gate.c), C.byref(up.c), C.byref(down.c), n_tokens, top_k))
+    return int(lib().uw_moe_workspace_bytes(C.byref(gate.c), C.byref(up.c), C.byref(down.c), _size_arg(n_tokens),
+                                            _size_arg(top_k)))
 
 
 def moe_block(gate: Experts, up: Experts, down: Experts, x, logits, top_k: int, y, ws: Workspace, residual=None,
@@ -728,7 +747,7 @@ def moe_block(gate: Experts, up: Experts, down: Experts, x, logits, top_k: int, 
         raise UwError(UW_ERR_INVALID_ARG, "gate, up and down on different devices")
     shape = (n_tokens, gate.cols)
     _call("uw_moe_block", dev, stream, C.byref(gate.c), C.byref(up.c), C.byref(down.c),
-          _tensor(logits, "logits", types, (n_tokens, len(gate)), dev), typ, top_k,
+          _tensor(logits, "logits", types, (n_tokens, len(gate)), dev), typ, _count(top_k, "top_k"),
           int(renormalize), _tensor(x, "x", _BF16, shape, dev), n_tokens,
           _tensor(residual, "residual", _BF16, shape, dev), _tensor(y, "y", _BF16, shape, dev),
           *_space(ws, dev))

@@ -278,6 +278,45 @@ def test_the_binding_checks_its_tensors():
     assert e.value.status == uw.UW_ERR_INVALID_ARG
 
 
+def test_counts_beyond_32_bits_are_not_wrapped(monkeypatch):
+    """2^32 + 2 is not 2: the library's counts have 32 bits."""
+    import torch
+    uw._need_torch()
+    big = 2**32 + 2
+    L = matrix().L
+    assert uw.route_workspace_bytes(2, 8, 2) > 0 and uw.epilogue_workspace_bytes(L, 2) > 0
+    for n in (big, 2**31, 2**40, -big):
+        assert uw.route_workspace_bytes(n, 8, 2) == uw.route_workspace_bytes(2, 8, n) == uw.route_workspace_bytes(2, n, 2) == 0
+        assert uw.epilogue_workspace_bytes(L, n) == 0
+
+    class Prepared:  # an Experts without a device
+        device, rows, cols = -1, 320, 256
+
+        def __init__(self, rows, cols):
+            self.rows, self.cols, self.c = rows, cols, table(rows=rows, cols=cols)
+
+        def __len__(self):
+            return 4
+
+    gate, down = Prepared(320, 256), Prepared(256, 320)
+    assert uw.grouped_workspace_bytes(gate, 2) > 0 and uw.moe_workspace_bytes(gate, gate, down, 2, 2) > 0
+    assert uw.grouped_workspace_bytes(gate, big) == 0
+    assert uw.moe_workspace_bytes(gate, gate, down, big, 2) == uw.moe_workspace_bytes(gate, gate, down, 2, big) == 0
+
+    monkeypatch.setattr(uw, "_call", lambda *a: pytest.fail("reached the library"))
+    x, logits = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(2, 4)
+    calls = [lambda: uw.moe_block(gate, gate, down, x, logits, big, x.clone(), None),
+             lambda: uw.moe_block(gate, gate, down, x, None, 2, x.clone(), None),
+             lambda: uw.moe_combine(torch.empty(big, 1, device="meta"), torch.zeros(2, 2, dtype=torch.int32),
+                                    torch.zeros(2, 2), torch.zeros(2, 1, dtype=torch.bfloat16)),
+             lambda: uw.Route(0, 8, big, device="cpu"),
+             lambda: uw._matrix_of(torch.empty(big, 64, device="meta"), "x")]
+    for i, call in enumerate(calls):
+        with pytest.raises(uw.UwError) as e:
+            call()
+        assert e.value.status == uw.UW_ERR_INVALID_ARG, i
+
+
 def test_the_plain_forms_themselves():
     """The references of the GPU tests at values worked by hand."""
     assert act_f64([-1.0, 2.0], "relu").tolist() == [0.0, 2.0]

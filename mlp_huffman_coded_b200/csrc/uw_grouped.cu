@@ -48,7 +48,6 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "uw_device.cuh"
 #include "uw_internal.h"
@@ -1615,20 +1614,26 @@ extern "C" uw_status uw_experts_init(const uw_matrix* const* mats, int32_t n_exp
                                      uw_experts* out, void* stream) {
   if (!mats || !table || !out || n_experts < 1 || n_experts > kMaxExperts || !aligned16(table)) return UW_ERR_INVALID_ARG;
   if (table_bytes < uw_experts_table_bytes(n_experts)) return UW_ERR_WORKSPACE_TOO_SMALL;
-  std::vector<ExpertDesc> host(static_cast<size_t>(n_experts));
+  ExpertDesc host[64];  // records go out in batches: no allocation that could throw
   for (int32_t e = 0; e < n_experts; ++e) {
     if (!mats[e]) return UW_ERR_INVALID_ARG;
     if (mats[e]->L.rows != mats[0]->L.rows || mats[e]->L.cols != mats[0]->L.cols) return UW_ERR_UNSUPPORTED_SHAPE;
-    const uw_status st = expert_desc(mats[e], &host[static_cast<size_t>(e)]);
+    const uw_status st = expert_desc(mats[e], &host[0]);
     if (st != UW_OK) return st;
   }
   DeviceInfo dev;
   uw_status st = device_info(&dev);
   if (st != UW_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(table, host.data(), host.size() * sizeof(ExpertDesc), cudaMemcpyHostToDevice, s) != cudaSuccess)
-    return UW_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return UW_ERR_CUDA;  // the host copy goes away
+  for (int32_t e0 = 0; e0 < n_experts; e0 += 64) {
+    const int32_t n = std::min(64, n_experts - e0);
+    for (int32_t i = 0; i < n; ++i)
+      if ((st = expert_desc(mats[e0 + i], &host[i])) != UW_OK) return st;
+    if (cudaMemcpyAsync(static_cast<ExpertDesc*>(table) + e0, host, static_cast<size_t>(n) * sizeof(ExpertDesc),
+                        cudaMemcpyHostToDevice, s) != cudaSuccess)
+      return UW_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return UW_ERR_CUDA;  // the host records change next
+  }
   std::memset(out, 0, sizeof(*out));
   out->n_experts = n_experts;
   out->rows = mats[0]->L.rows;

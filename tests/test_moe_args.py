@@ -175,6 +175,48 @@ def test_experts_refusals():
         uw.Experts([])
 
 
+def test_experts_init_allocates_nothing_that_could_throw(tmp_path):
+    """Nothing throws across the ABI: with an operator new that fails, the
+    call still returns a status (a child process, as a throw would end it)."""
+    import os
+    import subprocess
+    import sys
+    src, lib = tmp_path / "fail.cpp", tmp_path / "fail.so"
+    src.write_text("""
+        #include <cstdlib>
+        #include <new>
+        static bool fail = false;
+        extern "C" void set_fail(int on) { fail = on; }
+        void* operator new(std::size_t n) {
+          void* p = fail ? nullptr : std::malloc(n);
+          if (!p) throw std::bad_alloc();
+          return p;
+        }
+        void operator delete(void* p) noexcept { std::free(p); }
+        void operator delete(void* p, std::size_t) noexcept { std::free(p); }
+    """)
+    subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-o", str(lib), str(src)], check=True)
+    code = f"""
+import ctypes as C, sys
+sys.path[:0] = [{os.path.dirname(__file__)!r}, {os.path.dirname(os.path.dirname(uw.__file__))!r}]
+from mlp_huffman_coded_b200 import uw
+from test_moe_args import matrix, P
+h, m, out = C.CDLL({str(lib)!r}), matrix(), uw.ExpertTable()
+arr = (C.POINTER(uw.Matrix) * 1024)(*[C.pointer(m)] * 1024)
+f = uw.lib().uw_experts_init
+h.set_fail(1)
+st = f(arr, 1024, P, 0, C.byref(out), None), f(arr, 1024, P + 8, 1 << 20, C.byref(out), None)
+m.L.n_verbatim = -1  # refused before anything reaches a device
+st += (f(arr, 1024, P, 1 << 20, C.byref(out), None),)
+h.set_fail(0)
+print(*st)
+"""
+    env = dict(os.environ, LD_PRELOAD=str(lib), CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
+    assert r.stdout.split()[-3:] == [str(s) for s in (uw.UW_ERR_WORKSPACE_TOO_SMALL, uw.UW_ERR_INVALID_ARG, uw.UW_ERR_CORRUPT)]
+
+
 def test_experts_keep_the_tensors_their_table_points_to(monkeypatch):
     """Preparing a matrix again replaces its pack; the table still holds the
     old one's address, so Experts has to keep it alive."""

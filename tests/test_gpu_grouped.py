@@ -307,6 +307,66 @@ def test_more_than_two_to_the_31_output_values():
     del y
 
 
+def random_matrix(rows, cols, seed):
+    """BF16 matrix on the GPU: N(0, 0.02), one weight in 10^4 a hundredfold."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = torch.randn(rows, cols, generator=g, device="cuda") * 0.02
+    return torch.where(torch.rand(rows, cols, generator=g, device="cuda") < 1e-4, w * 100, w).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", [2104, 2101])  # 17 row tiles; the second: no row of y starts on 16 bytes but the first
+@pytest.mark.parametrize("scattered", [False, True])
+def test_epilogues_of_row_tile_pairs(rows, scattered):
+    """Twice the units from which pairs of row tiles share activations, the
+    last pair half empty, groups not multiples of 8.  The plain FP32 product
+    against float64; the epilogues against float64 forms of that same product,
+    so that only their own rounding is allowed."""
+    import torch
+    cols, counts = 16384, [1099, 1003, 0, 1195]
+    ws_ = [random_matrix(rows, cols, 1000 + e) for e in range(4)]
+    load = uw.Workspace(256)
+    ex = uw.Experts([uw.DeviceMatrix.encode_on_device(w).prepare_direct_palette(load, keep_idx4=False) for w in ws_])
+    off = offsets_of(counts)
+    n = int(off[-1])
+    x = synth.activations(n, cols, 1010)
+    r = np.random.default_rng(1011).permutation(n).astype(np.int32) if scattered else np.arange(n, dtype=np.int32)
+    xd, rd, offd = to_dev(x), to_dev(r) if scattered else None, to_dev(off)
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex, n))
+    z = torch.full((n, rows), 777.0, device="cuda")
+    uw.gemm_grouped(ex, xd, offd, z, ws, rows=rd)
+    ws.check()
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        for part in range(a, b, 400):  # float64 copies of x stay small
+            c = min(part + 400, b)
+            xe = f64(x[r[part:c]])
+            d = cols * 2.0 ** -23 * (xe.abs() @ ws_[e].double().abs().T)
+            assert float(((z[part:c].double() - xe @ ws_[e].double().T).abs() - d).max()) <= 0
+    bias = to_dev(synth.activations(4, rows, 1012))
+    res = to_dev(synth.activations(n, rows, 1013))
+    of_slot = torch.repeat_interleave(torch.arange(4, device="cuda"), torch.tensor(counts, device="cuda"))
+    bd, qd = bias.view(torch.bfloat16).double()[of_slot], res.view(torch.bfloat16).double()
+    for act, b, q, fp32 in (("gelu", bias, res, True), ("gelu", bias, res, False), ("none", bias, None, True),
+                            ("relu", None, res, False), ("none", None, None, False)):
+        v = z.double() + (0.0 if b is None else bd)
+        ref = {"gelu": lambda: 0.5 * v * torch.special.erfc(-v / 2 ** 0.5), "relu": lambda: v.clamp(min=0), "none": lambda: v}[act]()
+        # epilogue_bound with an exact sum: the bias's addition through a slope
+        # of at most 1.13, the activation's own error, the residual's addition
+        d = 1.13 * F32 * v.abs() + (64 * F32 * (v.abs() + ref.abs()) if act == "gelu" else 0.0)
+        ref = ref + (0.0 if q is None else qd)
+        d = d + F32 * ref.abs() + F32 * d + 1e-30
+        d = d if fp32 else d + HALF_ULP * (ref.abs() + d)
+        y = torch.full((n, rows), 777.0, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+        uw.gemm_grouped(ex, xd, offd, y, ws, rows=rd, bias=b, activation=act, residual=q)
+        ws.check()
+        assert float(((y.double() - ref).abs() - d).max()) <= 0, (act, fp32)
+        if q is not None and not fp32:  # in place on the residual
+            t = q.clone()
+            uw.gemm_grouped(ex, xd, offd, t, ws, rows=rd, bias=b, activation=act, residual=t)
+            ws.check()
+            assert torch.equal(t.view(torch.bfloat16), y)
+
+
 def test_millions_of_rows_of_a_small_matrix():
     """More rows than the narrow tiles that such a matrix prefers can count."""
     import torch

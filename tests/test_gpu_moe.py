@@ -51,6 +51,17 @@ def test_route_against_float64(T, E, k):
         check_route(run_route(logits, k, ren), logits, k, ren)
 
 
+@pytest.mark.parametrize("T", [1, 64, 65, 700])
+@pytest.mark.parametrize("E,k", [(9, 2), (16, 3), (17, 4), (32, 8), (65, 8), (128, 8), (129, 8), (257, 8), (1024, 32)])
+def test_route_on_both_sides_of_every_width(T, E, k):
+    """A lane's logits are 1, 2, 4, .. 32 of a token's: the borders between
+    them, and the largest router, with one block and with several."""
+    logits = np.random.default_rng(T * 2000 + E).standard_normal((T, E)).astype(np.float32) * 2
+    logits[T // 2, : E - 1] = -np.inf  # one expert left, the last
+    for ren in (True, False):
+        check_route(run_route(logits, k, ren), logits, k, ren)
+
+
 def test_route_bf16_logits_tie_often():
     logits = synth.bf16_bits_to_f32(synth.f32_to_bf16_bits(
         np.round(np.random.default_rng(3).standard_normal((300, 40)) * 4).astype(np.float32)))
@@ -371,6 +382,107 @@ def test_captured_block_replays_on_new_inputs(sparse_mlp):
         uw.moe_block(*ex, x, l, k, want, ws)
         ws.check()
         assert torch.equal(y, want)
+
+
+# the sizes of the framework's own blocks: waves, shared tiles, rows laid next to
+# each other, and row-tile pairs in the down product
+
+@pytest.fixture(scope="module")
+def full_size_mlp():
+    import torch
+    E, d, ffn = 8, 4096, 14336
+    load = uw.Workspace(256)
+
+    def experts(rows, cols, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        mats = [(torch.randn(rows, cols, generator=g, device="cuda") * 0.02).to(torch.bfloat16) for _ in range(E)]
+        return mats, uw.Experts([uw.DeviceMatrix.encode_on_device(w).prepare_direct_palette(load, keep_idx4=False)
+                                 for w in mats])
+
+    made = [experts(ffn, d, 710), experts(ffn, d, 711), experts(d, ffn, 712)]
+    yield [m for m, _ in made], [e for _, e in made]
+    del made
+    torch.cuda.empty_cache()
+
+
+def full_size_inputs(T, seed, E=8, d=4096):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device="cuda") + 0.7 * torch.randn(E, generator=g, device="cuda")
+    if T > 4:
+        logits[2] = -math.inf  # a padded token
+    return x, logits
+
+
+@pytest.mark.parametrize("T", [1, 32, 600])
+def test_full_size_block_against_float64(full_size_mlp, T):
+    import torch
+    (gs, us, ds), ex = full_size_mlp
+    x, logits = full_size_inputs(T, 720 + T)
+    k, E, K, F = 2, 8, 4096, 14336
+    res = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    y = torch.empty_like(x)
+    uw.moe_block(*ex, x, logits, k, y, ws, residual=res)
+    ws.check()
+    w, chosen, _, _, _ = route_ref(logits.cpu().numpy(), k)
+    w, chosen = torch.from_numpy(w).cuda(), torch.from_numpy(chosen).cuda()
+    xd, ref = x.double(), res.double()
+    bound = F32 * ref.abs()
+    for e in range(E):  # as block_ref, expert by expert
+        t, j = torch.nonzero(chosen == e, as_tuple=True)
+        if not t.numel():
+            continue
+        g, ag = xd[t] @ gs[e].double().T, xd[t].abs() @ gs[e].double().abs().T
+        u, au = xd[t] @ us[e].double().T, xd[t].abs() @ us[e].double().abs().T
+        dg, du = K * 2.0 ** -23 * ag, K * 2.0 ** -23 * au
+        s = g / (1 + torch.exp(-g))
+        h = s * u
+        dh = 1.1 * dg * u.abs() + s.abs() * du + 1.1 * dg * du + 16 * F32 * (g.abs() + s.abs()) * u.abs()
+        dh = dh + HALF_ULP * (h.abs() + dh)
+        part, ab = h @ ds[e].double().T, (h.abs() + dh) @ ds[e].double().abs().T
+        dpart = dh @ ds[e].double().abs().T + F * 2.0 ** -23 * ab
+        wt = w[t, j][:, None]
+        ref.index_add_(0, t, wt * part)
+        bound.index_add_(0, t, wt * dpart + (E + 184) * F32 * wt * (part.abs() + dpart) + 4 * F32 * wt * (part.abs() + dpart))
+    bound = bound + (k + 1) * F32 * ref.abs()
+    bound = bound + HALF_ULP * (ref.abs() + bound) + 1e-30
+    off = (y.double() - ref).abs()
+    assert float((off - bound).max()) <= 0
+    # the bounds add up worst cases of every sum; over all values the roundings
+    # of h and y count, each at most 2^-8 / sqrt(3) in the mean square
+    assert float(off.pow(2).mean().sqrt() / ref.pow(2).mean().sqrt()) <= HALF_ULP
+    if T > 4:
+        assert torch.equal(y[2], res[2])
+
+
+@pytest.mark.parametrize("T", [1, 32, 600])
+def test_full_size_blocks_in_a_row_equal_their_four_calls(full_size_mlp, T):
+    """Six blocks without a pause between them, each with a routing of its
+    own, against the four calls one by one with the device idle in between."""
+    import torch
+    _, ex = full_size_mlp
+    k, E, d, ffn = 2, 8, 4096, 14336
+    inputs = [full_size_inputs(T, 730 + i) for i in range(6)]
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    r = uw.Route(T, E, k)
+    h, parts = torch.empty(T * k, ffn, dtype=torch.bfloat16, device="cuda"), torch.empty(T * k, d, device="cuda")
+    want = []
+    for x, l in inputs:
+        y = torch.empty_like(x)
+        for call in (lambda: uw.moe_route(l, r, ws), lambda: uw.gemm_grouped_swiglu(ex[0], ex[1], x, r.offsets, h, ws, rows=r.rows),
+                     lambda: uw.gemm_grouped(ex[2], h, r.offsets, parts, ws), lambda: uw.moe_combine(parts, r.slots, r.weights, y)):
+            call()
+            torch.cuda.synchronize()
+        want.append(y)
+    ws.check()
+    for _ in range(3):
+        got = [torch.empty_like(x) for x, _ in inputs]
+        for (x, l), y in zip(inputs, got):
+            uw.moe_block(*ex, x, l, k, y, ws)
+        ws.check()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # ------------------------- refusals on the device ----------------------------

@@ -384,6 +384,89 @@ def test_captured_block_replays_on_new_inputs(sparse_mlp):
         assert torch.equal(y, want)
 
 
+def test_graphs_of_several_blocks_share_a_workspace(sparse_mlp):
+    """Two captured graphs of four blocks each, on one workspace, replayed in
+    turn without a pause."""
+    import torch
+    _, ex = sparse_mlp
+    T, k, d, E = 70, 2, ex[2].rows, len(ex[0])
+    side = torch.cuda.Stream()
+    x = to_dev(synth.activations(T, d, 695))
+    logits = torch.randn(2, 4, T, E, device="cuda") + 3 * torch.randn(2, 4, 1, E, device="cuda")
+    ws = uw.Workspace(uw.moe_workspace_bytes(*ex, T, k))
+    want = [empty_bf16(T, d) for _ in range(8)]
+    for l, y in zip(logits.view(8, T, E), want):
+        uw.moe_block(*ex, x, l, k, y, ws, residual=x)
+        torch.cuda.synchronize()
+    got = [empty_bf16(T, d) for _ in range(8)]
+    graphs = []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for l, y in zip(logits[i], got[4 * i:4 * i + 4]):
+                uw.moe_block(*ex, x, l, k, y, ws, residual=x)
+        graphs.append(graph)
+    for _ in range(5):
+        for y in got:
+            y.zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        ws.check()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_products_take_unaligned_slices(sparse_mlp):
+    """Bias, residual, offsets and row numbers one element into larger
+    tensors (x, y and the workspace are 16-byte aligned)."""
+    import torch
+    _, ex = sparse_mlp
+    E, n, ffn, d = len(ex[0]), 50, ex[0].rows, ex[0].cols
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        flat[1:] = t.flatten()
+        return flat[1:].view(t.shape)
+
+    x = to_dev(synth.activations(30, d, 696))
+    bias, res = to_dev(synth.activations(E, ffn, 697)), to_dev(synth.activations(n, ffn, 698))
+    off = torch.tensor([0, 20, 20, 23, 40, 41, 50], dtype=torch.int32, device="cuda")
+    rows = torch.randint(0, 30, (n,), dtype=torch.int32, device="cuda")
+    ws = uw.Workspace(uw.grouped_workspace_bytes(ex[0], n))
+    for fp32 in (False, True):
+        y = torch.zeros(n, ffn, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+        z = torch.zeros_like(y)
+        uw.gemm_grouped(ex[0], x, off, y, ws, rows=rows, bias=bias, activation="gelu_tanh", residual=res)
+        uw.gemm_grouped(ex[0], x, shifted(off), z, ws, rows=shifted(rows), bias=shifted(bias), activation="gelu_tanh",
+                        residual=shifted(res))
+        ws.check()
+        assert torch.equal(y, z) and bool(y.any())
+
+
+def test_route_of_a_million_tokens():
+    import torch
+    T, E, k = 1 << 20, 8, 3
+    g = torch.Generator(device="cuda").manual_seed(6)
+    logits = torch.argsort(torch.rand(T, E, device="cuda", generator=g), dim=1).float()  # 0 .. 7 in any order: no ties
+    logits[::5] = -math.inf
+    r = uw.Route(T, E, k)
+    ws = uw.Workspace(uw.route_workspace_bytes(T, E, k))
+    uw.moe_route(logits, r, ws)
+    ws.check()
+    chosen = torch.topk(logits, k, dim=1).indices.int()
+    chosen[::5] = -1
+    assert torch.equal(r.experts, chosen)
+    flat = torch.where(chosen < 0, E, chosen).flatten()
+    order = torch.sort(flat, stable=True).indices
+    n = int((flat < E).sum())
+    assert torch.equal(r.rows[:n].long(), order[:n] // k)
+    counts = torch.bincount(flat, minlength=E + 1)[:E]
+    assert r.offsets.tolist() == [0] + torch.cumsum(counts, 0).tolist()
+    slots = torch.full_like(flat, -1)
+    slots[order[:n]] = torch.arange(n, dtype=torch.int32, device="cuda")
+    assert torch.equal(r.slots.flatten(), slots)
+
+
 # the sizes of the framework's own blocks: waves, shared tiles, rows laid next to
 # each other, and row-tile pairs in the down product
 

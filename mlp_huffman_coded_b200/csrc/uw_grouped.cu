@@ -12,8 +12,9 @@
 //
 // What bounds it: with few rows per group, the bytes of the active groups'
 // packs (1.502 per weight plus 2 per verbatim weight); with many, the MMA
-// rate and the rebuild of each 128 x 64 weight tile (about 320 cycles of the
-// SM's issue slots, against 2 N cycles for the four MMAs of N columns).
+// rate and the rebuild of each 128 x 64 weight tile (193 ALU instructions per
+// warp at one per two cycles: 386 cycles, against 2 N cycles for the four MMAs
+// of N columns).
 //
 // Layout of the work:
 //  * W is the MMA's A operand (128 weight rows = 128 TMEM lanes), the rows of
@@ -415,10 +416,12 @@ __device__ __forceinline__ PaletteTables load_palette(const ExpertDesc* d) {
 // ------------------------------- epilogue ------------------------------------
 // FP32 throughout; the only rounding is the store's.  The GELU forms are
 // written so that they lose nothing where 1 + erf or 1 + tanh would cancel.
-// Divisions are the fast ones (2 units in the last place for divisors below
-// 2^126; theirs are at most 2).
+// Divisions are the fast ones: 2 units in the last place for divisors below
+// 2^126, 0 beyond.  What FP32 outputs can rely on is stated at uw_activation.
+
 // v / (1 + exp(-t)) for v and t of one sign, from e = exp(-|t|): exp(-t) leaves
 // the range where the result is still a normal number (SiLU(-90) = -7.4e-38).
+// The divisor is at most 2.
 __device__ __forceinline__ float times_sigmoid(float v, float t, float e) {
   return __fdividef(t > 0.0f ? v : v * e, 1.0f + e);
 }
@@ -429,10 +432,11 @@ __device__ __forceinline__ float silu_fast(float v) { return times_sigmoid(v, v,
 
 // Phi(-a) = erfc(a / sqrt 2) / 2 for a >= 0, as exp(-a^2 / 2) t P(t) with
 // z = a / sqrt 2, t = 1 / (1 + z / 2).  P: a minimax fit of erfcx(z) / t on z
-// in [0, 10] (relative error 4.3e-8; with the FP32 evaluation and the rounding
-// of the exponent, a Phi(-a) is within 1e-7 everywhere and Phi(-a) within 4e-6
-// relative down to 1e-37).  erfcf took twice as long: 664 rows of 7292 x 576
-// with GELU 41.9 us by it, 33.9 by this.
+// in [0, 10], relative error 4.3e-8.  Evaluated in FP32 it is within 44 2^-24,
+// the fast exponential within 2^-23 (2 + 0.6 a^2) and the rounding of its
+// argument within 2^-24 a^2 / 2, all relative: a Phi(-a) is within 1e-7
+// everywhere.  erfcf took twice as long: 664 rows of 7292 x 576 with GELU
+// 41.9 us by it, 33.9 by this.
 __device__ __forceinline__ float normal_tail(float a) {
   const float t = __fdividef(1.0f, 1.0f + 0.35355339f * a);
   float q = -0.05906814024f;
@@ -1270,7 +1274,8 @@ bool schedule_fits(int n_rows, int E, int cap, int n_mt, int KB) {
 // smallest, in units of one k-block of a tile (about 500 cycles).  Wide tiles
 // rebuild each weight tile less often, narrow ones give more tiles to spread
 // over the CTAs and less to carry through the epilogue.  A k-block costs the
-// larger of the rebuild (0.7) and the MMAs (2 cycles per column), the weights
+// larger of the rebuild (0.7; its 386 cycles of the ALU pipe would be 0.77) and the
+// MMAs (2 cycles per column), the weights
 // once from HBM 1.06 (per column tile when tiles are shared out and the
 // weights outgrow L2: their column tiles then come at different times); a
 // tile's epilogue 0.7 per 8 columns and 2, behind the next tile's k-blocks
